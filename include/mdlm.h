@@ -19,6 +19,12 @@
  * mixture's mdlm_corrupt_mixture + mdlm_compact_corrective;
  * mdlm_fused_head_ce_fwd_bwd_dw adds the head's own gradient.
  *
+ * Around the model that stands between the corrupted tokens and the final
+ * hidden states: mdlm_embed and mdlm_embed_grad (token embedding),
+ * mdlm_norm_fwd and mdlm_norm_bwd (final layer or RMS norm), and
+ * mdlm_ckpt8_save / _load (activation checkpoints in 8 bits, which
+ * mdlm_norm_fwd writes along the way and mdlm_norm_bwd_ckpt8 reads).
+ *
  * The method is defined on these pages:
  *   - LLaDA-8B-MDLM-LoRA model card, "Training" table, "Objective" row:
  *     one t ~ U(0,1) for each sequence, masking probability
@@ -505,6 +511,161 @@ int mdlm_fused_head_ce_fwd_bwd_dw(const void* hidden, const void* W,
 int mdlm_scale(const void* x, void* y, int32_t dtype, int64_t n, const float* scale,
                void* stream);
 
+/*
+ * mdlm_embed -- the model's input: one scaled table row per token.
+ *
+ * Defined by: LLaDA-8B-MDLM-LoRA card, Training table, "LoRA" row (the
+ * embeddings that stand before the model); diffusiongemma card (a model
+ * family whose embeddings are scaled).
+ *
+ *   out[i] = scale * table[ids[i]]
+ *
+ * the product in fp32, rounded once to `dtype`.  An id below 0 stands for no
+ * token (padding) and gives a row of zeros.  An id of V or more breaks a
+ * precondition: checking mode reports it, otherwise it gives zeros as well;
+ * neither reads outside the table.
+ *
+ *   ids         [n_tokens] int32 (xt of mdlm_corrupt, for one).
+ *   n_tokens    >= 0, below 2^31.
+ *   table       [V, H] row-major, element type `dtype`.
+ *   dtype       MDLM_BF16 or MDLM_F32.
+ *   V, H        > 0 (any H).
+ *   scale       finite.
+ *   out         [n_tokens, H], element type `dtype`.
+ * Pointers are aligned to their entries; nothing more is asked of them.
+ * Returns MDLM_OK, MDLM_EINVAL, MDLM_EUNSUPPORTED or MDLM_EHIP.
+ */
+int mdlm_embed(const int32_t* ids, int64_t n_tokens, const void* table, int32_t dtype,
+               int32_t V, int32_t H, float scale, void* out, void* stream);
+
+/*
+ * mdlm_embed_grad -- the gradient of mdlm_embed with respect to the table.
+ *
+ *   d_table[v] = [accumulate] d_table[v] + scale * sum over ids[i] = v of d_out[i]
+ *
+ * The tokens are sorted by id (ties by position), so each row's terms are
+ * summed in fp32 in an order that depends on the sizes alone: no atomics, the
+ * same bits on every run.  Ids outside [0, V) count for nothing.
+ *
+ *   ids, n_tokens, V, H, scale: as for mdlm_embed.
+ *   d_out       [n_tokens, H], element type `dtype` (MDLM_BF16 or MDLM_F32).
+ *   d_table     [V, H] float.  accumulate = 0: overwritten, zero where no
+ *               token points.  accumulate = 1: added to, rows without a token
+ *               left as they are (a table tied to the head: the dW of
+ *               mdlm_fused_head_ce_fwd_bwd_dw; or the gradients of several
+ *               micro-batches).
+ *   workspace   >= mdlm_embed_grad_workspace_bytes(n_tokens, H) bytes of
+ *               device memory, 256-byte aligned; contents on entry ignored.
+ * Calls sharing a workspace must not overlap.
+ * Returns MDLM_OK, MDLM_EINVAL, MDLM_EUNSUPPORTED, MDLM_EWORKSPACE or MDLM_EHIP.
+ */
+size_t mdlm_embed_grad_workspace_bytes(int64_t n_tokens, int32_t H);
+int mdlm_embed_grad(const int32_t* ids, int64_t n_tokens, const void* d_out, int32_t dtype,
+                    int32_t V, int32_t H, float scale, float* d_table, int32_t accumulate,
+                    void* workspace, size_t workspace_bytes, void* stream);
+
+/* Norms of mdlm_norm_fwd. */
+enum { MDLM_NORM_LAYER = 0, MDLM_NORM_RMS = 1 };
+
+/*
+ * mdlm_norm_fwd -- the norm that hands the model's last activation to the
+ * head, and with it, if wanted, an 8-bit checkpoint of that activation.
+ *
+ * Defined by: Axolotl docs, "Adapters, merging and inference" (the loss is
+ * taken from the final hidden states, which leave the model through this
+ * norm); LLaDA-8B-MDLM-LoRA card, Training table, "Precision" row (activation
+ * checkpoints).
+ *
+ *   LAYER: mean = mean(x_row), rstd = 1 / sqrt(mean((x_row - mean)^2) + eps)
+ *   RMS:   mean = 0,           rstd = 1 / sqrt(mean(x_row^2) + eps)
+ *   y = (x - mean) * rstd * weight + bias
+ *
+ * in fp32 throughout, y rounded once to `dtype`.
+ *
+ *   x           [n, H] row-major, element type `dtype`.
+ *   dtype       MDLM_BF16 or MDLM_F32.
+ *   n           >= 0 rows, below 2^31.
+ *   H           > 0; more than 16384 returns MDLM_EUNSUPPORTED.
+ *   kind        MDLM_NORM_LAYER or MDLM_NORM_RMS.
+ *   weight, bias  [H], element type `dtype`, or NULL (1 and 0).
+ *   eps         > 0, also as a float.
+ *   y           [n, H] out, element type `dtype`.
+ *   mean, rstd  [n] float out, or NULL (a call whose gradient nobody wants).
+ *               mean is not written for MDLM_NORM_RMS.
+ *   q, q_exp    the checkpoint of x (mdlm_ckpt8_save), or both NULL.
+ * Pointers are aligned to their entries; nothing more is asked of them.
+ * Returns MDLM_OK, MDLM_EINVAL, MDLM_EUNSUPPORTED or MDLM_EHIP.
+ */
+int mdlm_norm_fwd(const void* x, int32_t dtype, int64_t n, int32_t H, int32_t kind,
+                  const void* weight, const void* bias, double eps, void* y, float* mean,
+                  float* rstd, uint8_t* q, uint8_t* q_exp, void* stream);
+
+/*
+ * mdlm_norm_bwd -- the gradients of mdlm_norm_fwd.
+ * mdlm_norm_bwd_ckpt8 -- the same with x as the 8-bit checkpoint holds it
+ * (read as it lies; no restored copy is made).
+ *
+ *   xhat = (x - mean) * rstd,  g = dy * weight
+ *   dx       = rstd * (g - [LAYER] mean(g) - xhat * mean(g * xhat))
+ *   d_weight = [accumulate] d_weight + sum over rows of dy * xhat
+ *   d_bias   = [accumulate] d_bias   + sum over rows of dy
+ *
+ * in fp32, dx rounded once to `dtype`; the sums over rows are taken in an
+ * order that depends on the sizes alone.
+ *
+ *   dy          [n, H], element type `dtype` (d_hidden of the fused head).
+ *   mean, rstd  [n] as mdlm_norm_fwd left them (mean NULL for RMS).
+ *   dx          [n, H] out, element type `dtype`, or NULL.
+ *   d_weight, d_bias  [H] float out, or NULL (a frozen norm); with n = 0 they
+ *               are set to zero (accumulate = 0) or left as they are.
+ *   workspace   >= mdlm_norm_bwd_workspace_bytes(n, H) bytes of device
+ *               memory, 256-byte aligned; not needed without d_weight and
+ *               d_bias.
+ *   other arguments as for mdlm_norm_fwd.
+ * Calls sharing a workspace must not overlap.
+ * Returns MDLM_OK, MDLM_EINVAL (no output asked for, among others),
+ * MDLM_EUNSUPPORTED, MDLM_EWORKSPACE or MDLM_EHIP.
+ */
+size_t mdlm_norm_bwd_workspace_bytes(int64_t n, int32_t H);
+int mdlm_norm_bwd(const void* dy, const void* x, int32_t dtype, int64_t n, int32_t H,
+                  int32_t kind, const void* weight, const float* mean, const float* rstd,
+                  void* dx, float* d_weight, float* d_bias, int32_t accumulate, void* workspace,
+                  size_t workspace_bytes, void* stream);
+int mdlm_norm_bwd_ckpt8(const void* dy, const uint8_t* q, const uint8_t* q_exp, int32_t dtype,
+                        int64_t n, int32_t H, int32_t kind, const void* weight,
+                        const float* mean, const float* rstd, void* dx, float* d_weight,
+                        float* d_bias, int32_t accumulate, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
+/*
+ * mdlm_ckpt8_save, mdlm_ckpt8_load -- an activation kept in 8 bits between the
+ * forward and the backward pass, at a little over half of bf16's size.
+ *
+ * Defined by: LLaDA-8B-MDLM-LoRA card, Training table, "Precision" row
+ * (activation checkpoints; their format is this library's own).
+ *
+ * A row's entries are taken in blocks of 128 (the last may be shorter).  A
+ * block is stored as e4m3 values q (OCP 8-bit floating point, round to nearest
+ * even) and a byte b, and stands for q * 2^(b - 127): the least power of two,
+ * from 2^-127 up, under which the block's largest finite magnitude is at most
+ * 448, e4m3's largest value.  Dividing by it is exact, so an entry is off by
+ * at most 2^-4 of itself, or by 2^-10 * 2^(b - 127) where it is below
+ * 2^-6 * 2^(b - 127) (one that rounds up past the type's largest value comes
+ * back as an infinity).  Infinities and NaN are restored as NaN and do not
+ * touch the rest of their block.
+ *
+ *   x           [n, H] row-major, element type `dtype` (MDLM_BF16 or MDLM_F32;
+ *               the two calls need not use the same).
+ *   q           [n, H] bytes.
+ *   q_exp       [n, ceil(H / 128)] bytes.
+ *   n, H        n >= 0 and below 2^31, H > 0; n * ceil(H / 128) below 2^32.
+ * Returns MDLM_OK, MDLM_EINVAL, MDLM_EUNSUPPORTED or MDLM_EHIP.
+ */
+int mdlm_ckpt8_save(const void* x, int32_t dtype, int64_t n, int32_t H, uint8_t* q,
+                    uint8_t* q_exp, void* stream);
+int mdlm_ckpt8_load(const uint8_t* q, const uint8_t* q_exp, int32_t dtype, int64_t n, int32_t H,
+                    void* x, void* stream);
+
 /* Violation bits of the device-side precondition checks. */
 enum {
   MDLM_CHECK_OFFSETS = 1,    /* cu_seqlens not 0 = cu[0] <= ... <= cu[n_docs] = n_tokens */
@@ -512,7 +673,8 @@ enum {
   MDLM_CHECK_ROW_INDEX = 4,  /* a listed row index outside [0, n_tokens)                */
   MDLM_CHECK_TARGET = 8,     /* a listed target outside [0, V)                          */
   MDLM_CHECK_WEIGHT = 16,    /* a listed weight that is not finite                      */
-  MDLM_CHECK_PROB = 32       /* a p_doc entry outside (0, 1]                            */
+  MDLM_CHECK_PROB = 32,      /* a p_doc entry outside (0, 1]                            */
+  MDLM_CHECK_TOKEN = 64      /* a token id of V or more                                 */
 };
 
 /*
@@ -535,6 +697,8 @@ enum {
  *                       tgt[j] in [0, V) and w[j] finite (tgt and w may be
  *                       NULL: not checked).  Distinctness of the row indices
  *                       is not checked.
+ *   mdlm_check_tokens   ids [n_tokens] below V (a negative id, which stands
+ *                       for no token, passes).
  *   status              [1] int32 device word, 4-byte aligned.
  * Return MDLM_OK, MDLM_EINVAL (bad host arguments; nothing enqueued) or
  * MDLM_EHIP.
@@ -545,11 +709,14 @@ int mdlm_check_probs(const double* p_doc, int32_t n_docs, int32_t* status, void*
 int mdlm_check_rows(const int32_t* row_idx, const int32_t* tgt, const float* w,
                     const int32_t* n_rows, int64_t max_rows, int64_t n_tokens, int32_t V,
                     int32_t* status, void* stream);
+int mdlm_check_tokens(const int32_t* ids, int64_t n_tokens, int32_t V, int32_t* status,
+                      void* stream);
 
 /*
  * Checking mode.  With checking on, every entry point first checks its own
  * device inputs (as the calls above do: corruption its offsets; compaction
- * its offsets and noise levels; the fused head its row list), waits for the result on its stream, and returns MDLM_EINVAL with a
+ * its offsets and noise levels; the fused head its row list; the embedding
+ * and its gradient their token ids), waits for the result on its stream, and returns MDLM_EINVAL with a
  * message naming what is wrong -- enqueueing none of its own work -- if a
  * check fails.  This trades the calls' asynchrony for the checks: a call in
  * checking mode synchronises its stream, cannot be captured in a graph (it

@@ -38,6 +38,10 @@ MDLM_CHECK_ROW_INDEX = 4
 MDLM_CHECK_TARGET = 8
 MDLM_CHECK_WEIGHT = 16
 MDLM_CHECK_PROB = 32
+MDLM_CHECK_TOKEN = 64
+MDLM_NORM_LAYER = 0
+MDLM_NORM_RMS = 1
+MDLM_CKPT8_BLOCK = 128
 
 EXPORTED = (
     "mdlm_corrupt",
@@ -57,9 +61,19 @@ EXPORTED = (
     "mdlm_head_ce_dw_workspace_min_bytes",
     "mdlm_fused_head_ce_fwd_bwd_dw",
     "mdlm_scale",
+    "mdlm_embed",
+    "mdlm_embed_grad_workspace_bytes",
+    "mdlm_embed_grad",
+    "mdlm_norm_fwd",
+    "mdlm_norm_bwd_workspace_bytes",
+    "mdlm_norm_bwd",
+    "mdlm_norm_bwd_ckpt8",
+    "mdlm_ckpt8_save",
+    "mdlm_ckpt8_load",
     "mdlm_check_offsets",
     "mdlm_check_probs",
     "mdlm_check_rows",
+    "mdlm_check_tokens",
     "mdlm_set_checking",
     "mdlm_last_error",
     "mdlm_version",
@@ -128,6 +142,28 @@ def load():
     lib.mdlm_fused_head_ce_fwd_bwd_dw.restype = ctypes.c_int
     lib.mdlm_scale.argtypes = [vp, vp, i32, i64, vp, vp]
     lib.mdlm_scale.restype = ctypes.c_int
+    lib.mdlm_embed.argtypes = [vp, i64, vp, i32, i32, i32, f32, vp, vp]
+    lib.mdlm_embed.restype = ctypes.c_int
+    lib.mdlm_embed_grad_workspace_bytes.argtypes = [i64, i32]
+    lib.mdlm_embed_grad_workspace_bytes.restype = sz
+    lib.mdlm_embed_grad.argtypes = [vp, i64, vp, i32, i32, i32, f32, vp, i32, vp, sz, vp]
+    lib.mdlm_embed_grad.restype = ctypes.c_int
+    lib.mdlm_norm_fwd.argtypes = [vp, i32, i64, i32, i32, vp, vp, f64, vp, vp, vp, vp, vp, vp]
+    lib.mdlm_norm_fwd.restype = ctypes.c_int
+    lib.mdlm_norm_bwd_workspace_bytes.argtypes = [i64, i32]
+    lib.mdlm_norm_bwd_workspace_bytes.restype = sz
+    lib.mdlm_norm_bwd.argtypes = [vp, vp, i32, i64, i32, i32, vp, vp, vp, vp, vp, vp, i32, vp, sz,
+                                  vp]
+    lib.mdlm_norm_bwd.restype = ctypes.c_int
+    lib.mdlm_norm_bwd_ckpt8.argtypes = [vp, vp, vp, i32, i64, i32, i32, vp, vp, vp, vp, vp, vp,
+                                        i32, vp, sz, vp]
+    lib.mdlm_norm_bwd_ckpt8.restype = ctypes.c_int
+    lib.mdlm_ckpt8_save.argtypes = [vp, i32, i64, i32, vp, vp, vp]
+    lib.mdlm_ckpt8_save.restype = ctypes.c_int
+    lib.mdlm_ckpt8_load.argtypes = [vp, vp, i32, i64, i32, vp, vp]
+    lib.mdlm_ckpt8_load.restype = ctypes.c_int
+    lib.mdlm_check_tokens.argtypes = [vp, i64, i32, vp, vp]
+    lib.mdlm_check_tokens.restype = ctypes.c_int
     lib.mdlm_check_offsets.argtypes = [vp, i32, i64, vp, vp]
     lib.mdlm_check_offsets.restype = ctypes.c_int
     lib.mdlm_check_probs.argtypes = [vp, i32, vp, vp]
@@ -421,6 +457,213 @@ def mdlm_scale(x, y, scale, stream=None):
     _check(load().mdlm_scale(_ptr(x), _ptr(y), dt, x.numel(), _ptr(scale), _stream(stream)))
 
 
+def _same_device(dev, **tensors):
+    """Contiguous device tensors of the call, all on `dev`."""
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if t.device != dev:
+            raise ValueError(f"{name}: expected a tensor on {dev}, got {t.device}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name}: expected a contiguous tensor")
+
+
+def _rows(x, name):
+    """(n, H) of a tensor [..., H] taken as rows, and its element type code."""
+    if not x.is_cuda:
+        raise ValueError(f"{name}: expected a device tensor")
+    if x.dim() == 0:
+        raise ValueError(f"{name}: expected [..., H]")
+    H = x.shape[-1]
+    return (x.numel() // H if H else 0), H, dtype_code(x)
+
+
+def _shaped(t, shape, dtype, name):
+    if t is None:
+        return
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+class _On:
+    """The tensors' device as the current one, and the stream to launch on
+    (torch's current stream of that device unless one is given)."""
+
+    def __init__(self, dev, stream):
+        self.stream = stream  # None: the current one
+        if stream is None:
+            stream = torch.cuda.current_stream(dev)
+        elif stream.device != dev:
+            raise ValueError(f"stream: expected a stream of {dev}, got one of {stream.device}")
+        self.handle = stream.cuda_stream
+        self.guard = torch.cuda.device(dev) if dev.index != torch.cuda.current_device() else None
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        return self
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+    def scratch(self, dev, nbytes, workspace):
+        """(address, bytes, owner) of the caller's workspace, or of one allocated
+        on the launch stream for this call."""
+        if workspace is None and nbytes > 0:
+            with torch.cuda.stream(self.stream):
+                workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        if workspace is None:
+            return None, 0, None
+        if workspace.dtype != torch.uint8:
+            raise TypeError(f"workspace: expected torch.uint8, got {workspace.dtype}")
+        _same_device(dev, workspace=workspace)
+        return workspace.data_ptr(), workspace.numel(), workspace
+
+
+def mdlm_embed(ids, table, scale, out, stream=None):
+    """See mdlm_embed in include/mdlm.h: out[...] = scale * table[ids[...]].
+    `ids` int32 of any shape; `table` [V, H] and `out` [*ids.shape, H] bf16 or
+    float32."""
+    if table.dim() != 2:
+        raise ValueError("table: expected [V, H]")
+    V, H = table.shape
+    _, _, dt = _rows(table, "table")
+    dev = table.device
+    if ids.dtype != torch.int32:
+        raise TypeError(f"ids: expected torch.int32, got {ids.dtype}")
+    _shaped(out, (*ids.shape, H), table.dtype, "out")
+    _same_device(dev, ids=ids, table=table, out=out)
+    with _On(dev, stream) as on:
+        _check(load().mdlm_embed(ids.data_ptr(), ids.numel(), table.data_ptr(), dt, V, H,
+                                 float(scale), out.data_ptr(), on.handle))
+
+
+def mdlm_embed_grad_workspace_bytes(n_tokens, H):
+    return load().mdlm_embed_grad_workspace_bytes(int(n_tokens), int(H))
+
+
+def mdlm_embed_grad(ids, d_out, scale, d_table, accumulate=False, workspace=None, stream=None):
+    """See mdlm_embed_grad in include/mdlm.h: `d_out` [*ids.shape, H] bf16 or
+    float32, `d_table` [V, H] float32, overwritten or (accumulate) added to;
+    `workspace` a uint8 tensor, allocated for the call if None."""
+    if d_table.dim() != 2:
+        raise ValueError("d_table: expected [V, H]")
+    V, H = d_table.shape
+    if ids.dtype != torch.int32:
+        raise TypeError(f"ids: expected torch.int32, got {ids.dtype}")
+    n, _, dt = _rows(d_out, "d_out")
+    dev = d_out.device
+    _shaped(d_out, (*ids.shape, H), d_out.dtype, "d_out")
+    _shaped(d_table, (V, H), torch.float32, "d_table")
+    _same_device(dev, ids=ids, d_out=d_out, d_table=d_table)
+    lib = load()
+    with _On(dev, stream) as on:
+        ws, ws_bytes, _keep = on.scratch(dev, lib.mdlm_embed_grad_workspace_bytes(n, H), workspace)
+        _check(lib.mdlm_embed_grad(ids.data_ptr(), n, d_out.data_ptr(), dt, V, H, float(scale),
+                                   d_table.data_ptr(), 1 if accumulate else 0, ws, ws_bytes,
+                                   on.handle))
+
+
+def _ckpt8_shapes(q, q_exp, shape):
+    _shaped(q, shape, torch.uint8, "q")
+    _shaped(q_exp, (*shape[:-1], -(-shape[-1] // MDLM_CKPT8_BLOCK)), torch.uint8, "q_exp")
+
+
+def mdlm_norm_fwd(x, kind, weight, bias, eps, y, mean=None, rstd=None, q=None, q_exp=None,
+                  stream=None):
+    """See mdlm_norm_fwd in include/mdlm.h: `x`, `y` [..., H], `weight` and
+    `bias` [H] of x's type or None, `mean` and `rstd` float32 [...] or None,
+    `q` [..., H] and `q_exp` [..., ceil(H / 128)] uint8 or both None."""
+    n, H, dt = _rows(x, "x")
+    dev, lead = x.device, x.shape[:-1]
+    _shaped(weight, (H,), x.dtype, "weight")
+    _shaped(bias, (H,), x.dtype, "bias")
+    _shaped(y, x.shape, x.dtype, "y")
+    _shaped(mean, lead, torch.float32, "mean")
+    _shaped(rstd, lead, torch.float32, "rstd")
+    _ckpt8_shapes(q, q_exp, x.shape)
+    _same_device(dev, x=x, weight=weight, bias=bias, y=y, mean=mean, rstd=rstd, q=q, q_exp=q_exp)
+    with _On(dev, stream) as on:
+        _check(load().mdlm_norm_fwd(x.data_ptr(), dt, n, H, int(kind), _at(weight), _at(bias),
+                                    float(eps), y.data_ptr(), _at(mean), _at(rstd), _at(q),
+                                    _at(q_exp), on.handle))
+
+
+def mdlm_norm_bwd_workspace_bytes(n, H):
+    return load().mdlm_norm_bwd_workspace_bytes(int(n), int(H))
+
+
+def _norm_bwd(name, dy, source, kind, weight, mean, rstd, dx, d_weight, d_bias, accumulate,
+              workspace, stream):
+    n, H, dt = _rows(dy, "dy")
+    dev, lead = dy.device, dy.shape[:-1]
+    _shaped(weight, (H,), dy.dtype, "weight")
+    _shaped(mean, lead, torch.float32, "mean")
+    _shaped(rstd, lead, torch.float32, "rstd")
+    _shaped(dx, dy.shape, dy.dtype, "dx")
+    _shaped(d_weight, (H,), torch.float32, "d_weight")
+    _shaped(d_bias, (H,), torch.float32, "d_bias")
+    _same_device(dev, dy=dy, weight=weight, mean=mean, rstd=rstd, dx=dx, d_weight=d_weight,
+                 d_bias=d_bias, **source)
+    lib = load()
+    need = (lib.mdlm_norm_bwd_workspace_bytes(n, H)
+            if d_weight is not None or d_bias is not None else 0)
+    with _On(dev, stream) as on:
+        ws, ws_bytes, _keep = on.scratch(dev, need, workspace)
+        _check(getattr(lib, name)(dy.data_ptr(), *[_at(t) for t in source.values()], dt, n, H,
+                                  int(kind), _at(weight), _at(mean), _at(rstd), _at(dx),
+                                  _at(d_weight), _at(d_bias), 1 if accumulate else 0, ws,
+                                  ws_bytes, on.handle))
+
+
+def mdlm_norm_bwd(dy, x, kind, weight, mean, rstd, dx, d_weight=None, d_bias=None,
+                  accumulate=False, workspace=None, stream=None):
+    """See mdlm_norm_bwd in include/mdlm.h: `dy`, `x`, `dx` [..., H] of one type,
+    `mean` (None for RMS) and `rstd` as mdlm_norm_fwd left them, `d_weight` and
+    `d_bias` float32 [H]; outputs not wanted are None; `workspace` a uint8
+    tensor, allocated for the call if None."""
+    _shaped(x, dy.shape, dy.dtype, "x")
+    _norm_bwd("mdlm_norm_bwd", dy, {"x": x}, kind, weight, mean, rstd, dx, d_weight, d_bias,
+              accumulate, workspace, stream)
+
+
+def mdlm_norm_bwd_ckpt8(dy, q, q_exp, kind, weight, mean, rstd, dx, d_weight=None, d_bias=None,
+                        accumulate=False, workspace=None, stream=None):
+    """See mdlm_norm_bwd_ckpt8 in include/mdlm.h: mdlm_norm_bwd with x as the
+    8-bit checkpoint `q`, `q_exp` holds it."""
+    _ckpt8_shapes(q, q_exp, dy.shape)
+    _norm_bwd("mdlm_norm_bwd_ckpt8", dy, {"q": q, "q_exp": q_exp}, kind, weight, mean, rstd, dx,
+              d_weight, d_bias, accumulate, workspace, stream)
+
+
+def mdlm_ckpt8_save(x, q, q_exp, stream=None):
+    """See mdlm_ckpt8_save in include/mdlm.h: `x` [..., H] bf16 or float32 into
+    `q` [..., H] and `q_exp` [..., ceil(H / 128)] uint8."""
+    n, H, dt = _rows(x, "x")
+    _ckpt8_shapes(q, q_exp, x.shape)
+    _same_device(x.device, x=x, q=q, q_exp=q_exp)
+    with _On(x.device, stream) as on:
+        _check(load().mdlm_ckpt8_save(x.data_ptr(), dt, n, H, q.data_ptr(), q_exp.data_ptr(),
+                                      on.handle))
+
+
+def mdlm_ckpt8_load(q, q_exp, x, stream=None):
+    """See mdlm_ckpt8_load in include/mdlm.h: the checkpoint restored into `x`."""
+    n, H, dt = _rows(x, "x")
+    _ckpt8_shapes(q, q_exp, x.shape)
+    _same_device(x.device, x=x, q=q, q_exp=q_exp)
+    with _On(x.device, stream) as on:
+        _check(load().mdlm_ckpt8_load(q.data_ptr(), q_exp.data_ptr(), dt, n, H, x.data_ptr(),
+                                      on.handle))
+
+
 def mdlm_check_offsets(cu_seqlens, n_tokens, status, stream=None):
     """See mdlm_check_offsets in include/mdlm.h: ORs violation bits into the
     one-element int32 device tensor `status`."""
@@ -447,6 +690,14 @@ def mdlm_check_rows(row_idx, tgt, w, n_rows, max_rows, n_tokens, V, status, stre
     _check(load().mdlm_check_rows(_ptr(row_idx), _ptr(tgt), _ptr(w), _ptr(n_rows),
                                   int(max_rows), int(n_tokens), int(V), _ptr(status),
                                   _stream(stream)))
+
+
+def mdlm_check_tokens(ids, V, status, stream=None):
+    """See mdlm_check_tokens in include/mdlm.h."""
+    _need(ids, torch.int32, "ids")
+    _need(status, torch.int32, "status")
+    _check(load().mdlm_check_tokens(_ptr(ids), ids.numel(), int(V), _ptr(status),
+                                    _stream(stream)))
 
 
 def mdlm_set_checking(enable):

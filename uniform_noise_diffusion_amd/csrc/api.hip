@@ -49,13 +49,36 @@ static int check_row_list(const char* fn, const int32_t* row_idx, const int32_t*
   });
 }
 
+// Checking mode's step for entry points that take token ids.
+static int check_token_ids(const char* fn, const int32_t* ids, int64_t n, int32_t V,
+                           hipStream_t st) {
+  if (!checking_enabled() || n <= 0) return MDLM_OK;
+  return run_checks(fn, st,
+                    [&](int32_t* word) { return launch_check_tokens(ids, n, V, word, st); });
+}
+
+static size_t entry_bytes(int32_t dtype) { return dtype == MDLM_BF16 ? 2 : 4; }
+
+static bool misaligned(const void* p, size_t to) {
+  return reinterpret_cast<uintptr_t>(p) % to != 0;
+}
+
+// Sizes shared by the entry points that work on [n, H] rows.
+static int check_row_sizes(const char* fn, int32_t dtype, int64_t n, int32_t H) {
+  if (dtype != MDLM_F32 && dtype != MDLM_BF16)
+    return fail(MDLM_EINVAL, "%s: unknown dtype %d", fn, dtype);
+  if (n < 0 || H <= 0) return fail(MDLM_EINVAL, "%s: bad sizes n=%lld H=%d", fn, (long long)n, H);
+  if (n > INT32_MAX) return fail(MDLM_EUNSUPPORTED, "%s: n must be below 2^31", fn);
+  return MDLM_OK;
+}
+
 }  // namespace mdlm
 
 using namespace mdlm;
 
 extern "C" {
 
-int mdlm_version(void) { return (1 << 16) | 0; }
+int mdlm_version(void) { return (1 << 16) | 1; }
 
 const char* mdlm_last_error(void) { return g_error; }
 
@@ -426,6 +449,181 @@ int mdlm_scale(const void* x, void* y, int32_t dtype, int64_t n, const float* sc
   return MDLM_OK;
 }
 
+int mdlm_embed(const int32_t* ids, int64_t n_tokens, const void* table, int32_t dtype, int32_t V,
+               int32_t H, float scale, void* out, void* stream) {
+  clear_error();
+  const char* fn = "mdlm_embed";
+  const hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+  if (const int rc = check_row_sizes(fn, dtype, n_tokens, H)) return rc;
+  if (V <= 0) return fail(MDLM_EINVAL, "%s: V must be > 0", fn);
+  if (!isfinite(scale)) return fail(MDLM_EINVAL, "%s: scale must be finite", fn);
+  if (n_tokens > 0 && (!ids || !table || !out)) return fail(MDLM_EINVAL, "%s: null pointer", fn);
+  if (misaligned(ids, 4) || misaligned(table, entry_bytes(dtype)) ||
+      misaligned(out, entry_bytes(dtype)))
+    return fail(MDLM_EINVAL, "%s: a pointer is not aligned to its entries", fn);
+  if (const int rc = check_token_ids(fn, ids, n_tokens, V, st)) return rc;
+  if (launch_embed(ids, n_tokens, table, dtype, V, H, scale, out, st) != hipSuccess)
+    return check_launch(fn);
+  return MDLM_OK;
+}
+
+size_t mdlm_embed_grad_workspace_bytes(int64_t n_tokens, int32_t H) {
+  if (n_tokens > INT32_MAX) return 0;
+  return embed_grad_workspace_bytes(n_tokens, H);
+}
+
+int mdlm_embed_grad(const int32_t* ids, int64_t n_tokens, const void* d_out, int32_t dtype,
+                    int32_t V, int32_t H, float scale, float* d_table, int32_t accumulate,
+                    void* workspace, size_t workspace_bytes, void* stream) {
+  clear_error();
+  const char* fn = "mdlm_embed_grad";
+  const hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+  if (const int rc = check_row_sizes(fn, dtype, n_tokens, H)) return rc;
+  if (V <= 0) return fail(MDLM_EINVAL, "%s: V must be > 0", fn);
+  if (!isfinite(scale)) return fail(MDLM_EINVAL, "%s: scale must be finite", fn);
+  if (accumulate != 0 && accumulate != 1)
+    return fail(MDLM_EINVAL, "%s: accumulate must be 0 or 1", fn);
+  if (!d_table || (n_tokens > 0 && (!ids || !d_out)))
+    return fail(MDLM_EINVAL, "%s: null pointer", fn);
+  if (misaligned(ids, 4) || misaligned(d_out, entry_bytes(dtype)) || misaligned(d_table, 4))
+    return fail(MDLM_EINVAL, "%s: a pointer is not aligned to its entries", fn);
+  const size_t need = embed_grad_workspace_bytes(n_tokens, H);
+  if (need > 0 && (!workspace || workspace_bytes < need))
+    return fail(MDLM_EWORKSPACE, "%s: workspace of %zu bytes, need %zu", fn, workspace_bytes,
+                need);
+  if (need > 0 && misaligned(workspace, 256))
+    return fail(MDLM_EINVAL, "%s: workspace must be 256-byte aligned", fn);
+  if (const int rc = check_token_ids(fn, ids, n_tokens, V, st)) return rc;
+  if (launch_embed_grad(ids, n_tokens, d_out, dtype, V, H, scale, d_table, accumulate != 0,
+                        workspace, st) != hipSuccess)
+    return check_launch(fn);
+  return MDLM_OK;
+}
+
+// Sizes and kind of the norm's entry points.
+static int check_norm(const char* fn, int32_t dtype, int64_t n, int32_t H, int32_t kind) {
+  if (const int rc = check_row_sizes(fn, dtype, n, H)) return rc;
+  if (H > kNormMaxH)
+    return fail(MDLM_EUNSUPPORTED, "%s: H = %d exceeds %d", fn, H, kNormMaxH);
+  if (kind != MDLM_NORM_LAYER && kind != MDLM_NORM_RMS)
+    return fail(MDLM_EINVAL, "%s: unknown norm %d", fn, kind);
+  return MDLM_OK;
+}
+
+int mdlm_norm_fwd(const void* x, int32_t dtype, int64_t n, int32_t H, int32_t kind,
+                  const void* weight, const void* bias, double eps, void* y, float* mean,
+                  float* rstd, uint8_t* q, uint8_t* q_exp, void* stream) {
+  clear_error();
+  const char* fn = "mdlm_norm_fwd";
+  if (const int rc = check_norm(fn, dtype, n, H, kind)) return rc;
+  if (!(eps > 0.0) || !((float)eps > 0.f) || !isfinite((float)eps))
+    return fail(MDLM_EINVAL, "%s: eps must be a positive float", fn);
+  if (n > 0 && (!x || !y)) return fail(MDLM_EINVAL, "%s: null pointer", fn);
+  if ((q == nullptr) != (q_exp == nullptr))
+    return fail(MDLM_EINVAL, "%s: q and q_exp are given together or not at all", fn);
+  const size_t to = entry_bytes(dtype);
+  if (misaligned(x, to) || misaligned(weight, to) || misaligned(bias, to) || misaligned(y, to) ||
+      misaligned(mean, 4) || misaligned(rstd, 4))
+    return fail(MDLM_EINVAL, "%s: a pointer is not aligned to its entries", fn);
+  if (launch_norm_fwd(x, dtype, n, H, kind, weight, bias, eps, y, mean, rstd, q, q_exp,
+                      reinterpret_cast<hipStream_t>(stream)) != hipSuccess)
+    return check_launch(fn);
+  return MDLM_OK;
+}
+
+size_t mdlm_norm_bwd_workspace_bytes(int64_t n, int32_t H) {
+  if (n > INT32_MAX) return 0;
+  return norm_bwd_workspace_bytes(n, H);
+}
+
+// Shared checks and launch of both backward entry points.
+static int norm_bwd_common(const char* fn, const void* dy, bool from_x, const void* x,
+                           const uint8_t* q, const uint8_t* q_exp, int32_t dtype, int64_t n,
+                           int32_t H, int32_t kind, const void* weight, const float* mean,
+                           const float* rstd, void* dx, float* d_weight, float* d_bias,
+                           int32_t accumulate, void* workspace, size_t workspace_bytes,
+                           void* stream) {
+  if (const int rc = check_norm(fn, dtype, n, H, kind)) return rc;
+  if (accumulate != 0 && accumulate != 1)
+    return fail(MDLM_EINVAL, "%s: accumulate must be 0 or 1", fn);
+  if (n > 0 && (!dy || !rstd || (kind == MDLM_NORM_LAYER && !mean) ||
+                (from_x ? !x : !q || !q_exp)))
+    return fail(MDLM_EINVAL, "%s: null input pointer", fn);
+  if (n > 0 && !dx && !d_weight && !d_bias)
+    return fail(MDLM_EINVAL, "%s: no gradient is asked for", fn);
+  const size_t to = entry_bytes(dtype);
+  if (misaligned(dy, to) || misaligned(x, to) || misaligned(weight, to) || misaligned(mean, 4) ||
+      misaligned(rstd, 4) || misaligned(dx, to) || misaligned(d_weight, 4) ||
+      misaligned(d_bias, 4))
+    return fail(MDLM_EINVAL, "%s: a pointer is not aligned to its entries", fn);
+  const size_t need = d_weight || d_bias ? norm_bwd_workspace_bytes(n, H) : 0;
+  if (need > 0 && (!workspace || workspace_bytes < need))
+    return fail(MDLM_EWORKSPACE, "%s: workspace of %zu bytes, need %zu", fn, workspace_bytes,
+                need);
+  if (need > 0 && misaligned(workspace, 256))
+    return fail(MDLM_EINVAL, "%s: workspace must be 256-byte aligned", fn);
+  if (launch_norm_bwd(dy, x, q, q_exp, dtype, n, H, kind, weight, mean, rstd, dx, d_weight,
+                      d_bias, accumulate != 0, workspace,
+                      reinterpret_cast<hipStream_t>(stream)) != hipSuccess)
+    return check_launch(fn);
+  return MDLM_OK;
+}
+
+int mdlm_norm_bwd(const void* dy, const void* x, int32_t dtype, int64_t n, int32_t H,
+                  int32_t kind, const void* weight, const float* mean, const float* rstd,
+                  void* dx, float* d_weight, float* d_bias, int32_t accumulate, void* workspace,
+                  size_t workspace_bytes, void* stream) {
+  clear_error();
+  return norm_bwd_common("mdlm_norm_bwd", dy, true, x, nullptr, nullptr, dtype, n, H, kind,
+                         weight, mean, rstd, dx, d_weight, d_bias, accumulate, workspace,
+                         workspace_bytes, stream);
+}
+
+int mdlm_norm_bwd_ckpt8(const void* dy, const uint8_t* q, const uint8_t* q_exp, int32_t dtype,
+                        int64_t n, int32_t H, int32_t kind, const void* weight,
+                        const float* mean, const float* rstd, void* dx, float* d_weight,
+                        float* d_bias, int32_t accumulate, void* workspace,
+                        size_t workspace_bytes, void* stream) {
+  clear_error();
+  return norm_bwd_common("mdlm_norm_bwd_ckpt8", dy, false, nullptr, q, q_exp, dtype, n, H, kind,
+                         weight, mean, rstd, dx, d_weight, d_bias, accumulate, workspace,
+                         workspace_bytes, stream);
+}
+
+// Checks of both checkpoint entry points; x's end is the output of one.
+static int check_ckpt8(const char* fn, const void* x, int32_t dtype, int64_t n, int32_t H,
+                       const uint8_t* q, const uint8_t* q_exp) {
+  if (const int rc = check_row_sizes(fn, dtype, n, H)) return rc;
+  if (n * (((int64_t)H + 127) / 128) > UINT32_MAX)
+    return fail(MDLM_EUNSUPPORTED, "%s: 2^32 or more blocks of 128", fn);
+  if (n > 0 && (!x || !q || !q_exp)) return fail(MDLM_EINVAL, "%s: null pointer", fn);
+  if (misaligned(x, entry_bytes(dtype)))
+    return fail(MDLM_EINVAL, "%s: x is not aligned to its entries", fn);
+  return MDLM_OK;
+}
+
+int mdlm_ckpt8_save(const void* x, int32_t dtype, int64_t n, int32_t H, uint8_t* q,
+                    uint8_t* q_exp, void* stream) {
+  clear_error();
+  const char* fn = "mdlm_ckpt8_save";
+  if (const int rc = check_ckpt8(fn, x, dtype, n, H, q, q_exp)) return rc;
+  if (launch_ckpt8_save(x, dtype, n, H, q, q_exp, reinterpret_cast<hipStream_t>(stream)) !=
+      hipSuccess)
+    return check_launch(fn);
+  return MDLM_OK;
+}
+
+int mdlm_ckpt8_load(const uint8_t* q, const uint8_t* q_exp, int32_t dtype, int64_t n, int32_t H,
+                    void* x, void* stream) {
+  clear_error();
+  const char* fn = "mdlm_ckpt8_load";
+  if (const int rc = check_ckpt8(fn, x, dtype, n, H, q, q_exp)) return rc;
+  if (launch_ckpt8_load(q, q_exp, dtype, n, H, x, reinterpret_cast<hipStream_t>(stream)) !=
+      hipSuccess)
+    return check_launch(fn);
+  return MDLM_OK;
+}
+
 int mdlm_check_offsets(const int32_t* cu_seqlens, int32_t n_docs, int64_t n_tokens,
                        int32_t* status, void* stream) {
   clear_error();
@@ -459,6 +657,18 @@ int mdlm_check_rows(const int32_t* row_idx, const int32_t* tgt, const float* w,
     return fail(MDLM_EINVAL, "%s: null pointer", fn);
   if (launch_check_rows(row_idx, tgt, w, n_rows, max_rows, n_tokens, V, status,
                         reinterpret_cast<hipStream_t>(stream)) != hipSuccess)
+    return check_launch(fn);
+  return MDLM_OK;
+}
+
+int mdlm_check_tokens(const int32_t* ids, int64_t n_tokens, int32_t V, int32_t* status,
+                      void* stream) {
+  clear_error();
+  const char* fn = "mdlm_check_tokens";
+  if (n_tokens < 0 || V <= 0) return fail(MDLM_EINVAL, "%s: bad sizes", fn);
+  if (!status || (n_tokens > 0 && !ids)) return fail(MDLM_EINVAL, "%s: null pointer", fn);
+  if (launch_check_tokens(ids, n_tokens, V, status, reinterpret_cast<hipStream_t>(stream)) !=
+      hipSuccess)
     return check_launch(fn);
   return MDLM_OK;
 }

@@ -92,6 +92,17 @@ check_rows_kernel(const int32_t* __restrict__ row_idx, const int32_t* __restrict
   }
 }
 
+// Token ids below V (a negative id stands for no token).
+__global__ void __launch_bounds__(kThreads)
+check_tokens_kernel(const int32_t* __restrict__ ids, int64_t n, int32_t V,
+                    int32_t* __restrict__ status) {
+  for (int64_t base = (int64_t)blockIdx.x * kThreads; base < n;
+       base += (int64_t)gridDim.x * kThreads) {
+    const int64_t i = base + threadIdx.x;
+    report(i < n && ids[i] >= V, MDLM_CHECK_TOKEN, status);
+  }
+}
+
 __global__ void clear_word_kernel(int32_t* p) { *p = 0; }
 
 unsigned blocks_for(int64_t n) {
@@ -120,6 +131,13 @@ hipError_t launch_check_rows(const int32_t* row_idx, const int32_t* tgt, const f
   check_rows_kernel<<<blocks_for(max_rows), kThreads, 0, stream>>>(row_idx, tgt, w, n_rows,
                                                                    max_rows, n_tokens, V,
                                                                    status);
+  return hipGetLastError();
+}
+
+hipError_t launch_check_tokens(const int32_t* ids, int64_t n, int32_t V, int32_t* status,
+                               hipStream_t stream) {
+  if (n <= 0) return hipSuccess;
+  check_tokens_kernel<<<blocks_for(n), kThreads, 0, stream>>>(ids, n, V, status);
   return hipGetLastError();
 }
 
@@ -169,7 +187,8 @@ int run_checks(const char* fn, hipStream_t stream, const CheckEnqueue& enqueue) 
     const char* name;
   } names[] = {{MDLM_CHECK_OFFSETS, "cu_seqlens"},   {MDLM_CHECK_ROW_COUNT, "n_rows"},
                {MDLM_CHECK_ROW_INDEX, "row_idx"},    {MDLM_CHECK_TARGET, "tgt"},
-               {MDLM_CHECK_WEIGHT, "w"},             {MDLM_CHECK_PROB, "p_doc"}};
+               {MDLM_CHECK_WEIGHT, "w"},             {MDLM_CHECK_PROB, "p_doc"},
+               {MDLM_CHECK_TOKEN, "ids"}};
   for (const auto& n : names)
     if (bits & n.bit) {
       if (what[0]) strncat(what, ", ", sizeof what - strlen(what) - 1);

@@ -211,6 +211,30 @@ hipError_t launch_head_ce(const HeadCeArgs& a, hipStream_t stream);
 hipError_t launch_scale(const void* x, void* y, int32_t dtype, int64_t n, const float* scale,
                         hipStream_t stream);
 
+// ---- the model's ends (embed.hip, norm.hip, ckpt8.hip) ---------------------
+// out[i] = scale * table[ids[i]] (zeros for an id outside [0, V))
+hipError_t launch_embed(const int32_t* ids, int64_t n, const void* table, int32_t dtype,
+                        int32_t V, int32_t H, float scale, void* out, hipStream_t stream);
+size_t embed_grad_workspace_bytes(int64_t n, int32_t H);
+hipError_t launch_embed_grad(const int32_t* ids, int64_t n, const void* d_out, int32_t dtype,
+                             int32_t V, int32_t H, float scale, float* d_table, bool accumulate,
+                             void* workspace, hipStream_t stream);
+// Rows of at most kNormMaxH entries (16 waves hold one row in registers).
+constexpr int32_t kNormMaxH = 16384;
+hipError_t launch_norm_fwd(const void* x, int32_t dtype, int64_t n, int32_t H, int32_t kind,
+                           const void* weight, const void* bias, double eps, void* y, float* mean,
+                           float* rstd, uint8_t* q, uint8_t* q_exp, hipStream_t stream);
+size_t norm_bwd_workspace_bytes(int64_t n, int32_t H);
+// x, or (x null) the checkpoint q, q_exp
+hipError_t launch_norm_bwd(const void* dy, const void* x, const uint8_t* q, const uint8_t* q_exp,
+                           int32_t dtype, int64_t n, int32_t H, int32_t kind, const void* weight,
+                           const float* mean, const float* rstd, void* dx, float* d_weight,
+                           float* d_bias, bool accumulate, void* workspace, hipStream_t stream);
+hipError_t launch_ckpt8_save(const void* x, int32_t dtype, int64_t n, int32_t H, uint8_t* q,
+                             uint8_t* q_exp, hipStream_t stream);
+hipError_t launch_ckpt8_load(const uint8_t* q, const uint8_t* q_exp, int32_t dtype, int64_t n,
+                             int32_t H, void* x, hipStream_t stream);
+
 // ---- device-side precondition checks (check.hip) -------------------------
 // Each ORs MDLM_CHECK_* bits into *status; inputs are only read.
 hipError_t launch_check_offsets(const int32_t* cu, int32_t n_docs, int64_t n, int32_t* status,
@@ -220,6 +244,8 @@ hipError_t launch_check_probs(const double* p, int32_t n_docs, int32_t* status,
 hipError_t launch_check_rows(const int32_t* row_idx, const int32_t* tgt, const float* w,
                              const int32_t* n_rows, int64_t max_rows, int64_t n_tokens,
                              int32_t V, int32_t* status, hipStream_t stream);
+hipError_t launch_check_tokens(const int32_t* ids, int64_t n, int32_t V, int32_t* status,
+                               hipStream_t stream);
 // Checking mode: off unless MDLM_CHECK is set (not "0") at the first query,
 // or switched by set_checking (which returns the previous setting).
 bool checking_enabled();

@@ -89,3 +89,83 @@ class MdlmLossStep:
         self.corrupt(x0, cu_seqlens, seed, eps, noise, mask_id, rand_vocab, stream)
         self.compact(x0, cu_seqlens, align, stream)
         self.head_ce(hidden, W, softcap, stream, want_grad, row_ce)
+
+
+class MdlmTrainStep(MdlmLossStep):
+    """A training step of a model whose embedding, final norm and head are
+    trained, the model's own layers running between embed() and final_norm()
+    and between norm_grad() and embed_grad():
+
+        corrupt, compact   ->  embed          ->  the model's layers
+        ->  final_norm     ->  head_ce_dw     ->  norm_grad
+        ->  the layers' backward              ->  embed_grad
+
+    final_norm() keeps its input as an 8-bit checkpoint, so the caller need not
+    hold it until norm_grad().  With a tied head (`tied`) the table is the head:
+    embed_grad() adds to the `dW` that head_ce_dw() wrote; otherwise it writes
+    `d_table`.  bf16, as the trained head is."""
+
+    def __init__(self, n_tokens, n_docs, H, V, norm_kind=B.MDLM_NORM_RMS, norm_eps=1e-5,
+                 norm_bias=False, embed_scale=1.0, tied=True, device="cuda"):
+        dw_bytes = B.mdlm_head_ce_dw_workspace_bytes(n_tokens, H, V)
+        super().__init__(n_tokens, n_docs, H, V, device=device, head_workspace_bytes=dw_bytes)
+        dev = self.xt.device
+        f32 = dict(dtype=torch.float32, device=dev)
+        u8 = dict(dtype=torch.uint8, device=dev)
+        self.norm_kind, self.norm_eps, self.embed_scale = norm_kind, norm_eps, embed_scale
+        self.embedded = torch.empty((n_tokens, H), dtype=self.dtype, device=dev)
+        self.hidden = torch.empty_like(self.embedded)
+        self.mean = torch.empty(n_tokens, **f32) if norm_kind == B.MDLM_NORM_LAYER else None
+        self.rstd = torch.empty(n_tokens, **f32)
+        self.q = torch.empty((n_tokens, H), **u8)
+        self.q_exp = torch.empty((n_tokens, -(-H // B.MDLM_CKPT8_BLOCK)), **u8)
+        self.d_last = torch.empty_like(self.embedded)
+        self.d_norm_weight = torch.empty(H, **f32)
+        self.d_norm_bias = torch.empty(H, **f32) if norm_bias else None
+        self.dW = torch.empty((V, H), **f32)
+        self.tied = tied
+        self.d_table = self.dW if tied else torch.empty((V, H), **f32)
+        self.norm_ws = torch.empty(max(B.mdlm_norm_bwd_workspace_bytes(n_tokens, H), 1), **u8)
+        self.embed_ws = torch.empty(max(B.mdlm_embed_grad_workspace_bytes(n_tokens, H), 1), **u8)
+        self._norm_weight = None
+
+    def embed(self, table, stream=None):
+        """The corrupted tokens' embeddings into `embedded`."""
+        B.mdlm_embed(self.xt, table, self.embed_scale, self.embedded, stream)
+        return self.embedded
+
+    def final_norm(self, x, weight, bias=None, stream=None):
+        """The final norm of the model's last activation into `hidden`; x is kept
+        as an 8-bit checkpoint."""
+        if (bias is None) != (self.d_norm_bias is None):
+            raise ValueError("bias: given exactly when the step was made with norm_bias=True")
+        self._norm_weight = weight
+        B.mdlm_norm_fwd(x, self.norm_kind, weight, bias, self.norm_eps, self.hidden, self.mean,
+                        self.rstd, self.q, self.q_exp, stream)
+        return self.hidden
+
+    def head_ce_dw(self, W, softcap=0.0, stream=None):
+        """Loss, `d_hidden` and the head's gradient `dW` from `hidden`."""
+        B.mdlm_fused_head_ce_fwd_bwd_dw(self.hidden, W, self.row_idx, self.tgt, self.w,
+                                        self.n_rows, self.n_tokens, softcap, self.loss,
+                                        self.row_ce, self.d_hidden, self.dW, self.head_ws, stream)
+        return self.loss
+
+    def norm_grad(self, stream=None):
+        """`d_last` (the gradient that enters the model's layers) and the norm's
+        own gradients from `d_hidden` and the checkpoint of the last
+        final_norm()."""
+        if self._norm_weight is None:
+            raise RuntimeError("norm_grad() follows final_norm()")
+        B.mdlm_norm_bwd_ckpt8(self.d_hidden, self.q, self.q_exp, self.norm_kind,
+                              self._norm_weight, self.mean, self.rstd, self.d_last,
+                              self.d_norm_weight, self.d_norm_bias, workspace=self.norm_ws,
+                              stream=stream)
+        return self.d_last
+
+    def embed_grad(self, d_embedded, stream=None):
+        """The table's gradient from the gradient of `embedded`: added to `dW`
+        (tied) or written to `d_table`."""
+        B.mdlm_embed_grad(self.xt, d_embedded, self.embed_scale, self.d_table,
+                          accumulate=self.tied, workspace=self.embed_ws, stream=stream)
+        return self.d_table
