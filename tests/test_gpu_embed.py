@@ -57,6 +57,8 @@ def draw_ids(rng, kind, n, V):
         ids = rng.permutation(max(n, V))[:n] % V
     elif kind == "few":  # long runs that start and end inside chunks
         ids = rng.integers(0, min(V, 5), n)
+    elif kind == "uniform":
+        ids = rng.integers(0, V, n)
     elif kind == "none":  # no token at all
         ids = rng.choice([-1, -7, V, V + 100], n)
     else:  # "padded": a tail without tokens, some ids too large
@@ -100,7 +102,12 @@ def test_embed_grad_runs(dtype, accumulate, kind, n):
     (16384, 40, 9000, torch.bfloat16, "absorb"),   # sixteen tiles: one merge
     (16385, 40, 9000, torch.bfloat16, "absorb"),   # two merges, the longer chunks
     (40000, 33, 300, torch.float32, "few"),
+    (20000, 40, 60, torch.float32, "uniform"),     # hundreds of cut runs
+    (33000, 300, 9000, torch.bfloat16, "absorb"),  # a cut run of 500 chunks
+    (8193, 24, 400, torch.float32, "absorb"),      # the sorted runs merged in LDS
+    (32769, 16, 40000, torch.float32, "padded"),   # and in memory
     (70001, 16, 70000, torch.float32, "distinct"),
+    (600000, 8, 5000, torch.float32, "absorb"),    # two merges in memory
     (3000, 1, 50, torch.float32, "few"),
     (300, 1001, 400, torch.bfloat16, "padded"),
     (200, 2816, 90, torch.bfloat16, "few"),
