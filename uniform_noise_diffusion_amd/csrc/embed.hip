@@ -533,7 +533,12 @@ join_runs_kernel(const int32_t* __restrict__ sid, int64_t n, int32_t V, int32_t 
 int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 
 // Entries of the sorted list per chunk.
-int chunk_of(int64_t n) { return n <= 16384 ? 16 : kMaxChunk; }
+int chunk_of(int64_t n, int32_t H) {
+  const int64_t slabs = (H + 511) / 512;
+  int C = kMaxChunk;
+  while (C > 4 && n * slabs < (int64_t)C * 2048) C /= 2;
+  return C;
+}
 
 int64_t pitch_of(int32_t H) { return round_up(H, 8); }
 
@@ -542,7 +547,7 @@ void run_sum(const int32_t* sid, const int32_t* spos, int64_t n, int32_t V, int3
              const void* d_out, float scale, float* d_table, bool accumulate, float* part,
              uint8_t* cut, hipStream_t stream) {
   const T* g = reinterpret_cast<const T*>(d_out);
-  const int C = chunk_of(n);
+  const int C = chunk_of(n, H);
   const int slabs = (H + 511) / 512;
   const int64_t units = (n + C - 1) / C * slabs;
   const unsigned grid = (unsigned)std::min<int64_t>((units + kWaves - 1) / kWaves, kMaxBlocks);
@@ -584,7 +589,7 @@ hipError_t launch_embed(const int32_t* ids, int64_t n, const void* table, int32_
 // a byte per chunk, then two partial rows per chunk.
 size_t embed_grad_workspace_bytes(int64_t n, int32_t H) {
   if (n <= 0 || H <= 0) return 0;
-  const int C = chunk_of(n);
+  const int C = chunk_of(n, H);
   const int64_t chunks = (n + C - 1) / C;
   return (size_t)(4 * round_up(4 * n, 256) + round_up(chunks, 256) +
                   chunks * 2 * pitch_of(H) * 4);
@@ -599,7 +604,7 @@ hipError_t launch_embed_grad(const int32_t* ids, int64_t n, const void* d_out, i
   int32_t* sid[2] = {reinterpret_cast<int32_t*>(ws), reinterpret_cast<int32_t*>(ws + 2 * list)};
   int32_t* spos[2] = {reinterpret_cast<int32_t*>(ws + list),
                       reinterpret_cast<int32_t*>(ws + 3 * list)};
-  const int C = chunk_of(n);
+  const int C = chunk_of(n, H);
   uint8_t* cut = reinterpret_cast<uint8_t*>(ws + 4 * list);
   float* part = reinterpret_cast<float*>(ws + 4 * list + round_up((n + C - 1) / C, 256));
   if (!accumulate) {

@@ -15,6 +15,7 @@ typedef __bf16 bf16_t;
 // These types carry that alignment, and the compiler still emits one wide
 // instruction for each.
 typedef uint32_t u32x4_a2 __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t u32x4_a1 __attribute__((ext_vector_type(4), aligned(1)));
 typedef uint32_t u32x2_a1 __attribute__((ext_vector_type(2), aligned(1)));
 typedef float f32x4_a4 __attribute__((ext_vector_type(4), aligned(4)));
 
@@ -82,11 +83,12 @@ __device__ __forceinline__ void widen(const Raw8<float>& r, float v[8]) {
   for (int i = 0; i < 8; ++i) v[i] = r.w[i];
 }
 
-// fp32 -> entries, rounded to nearest even.
+// fp32 -> entries, rounded to nearest even (one instruction for two).
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  const bf16_t a = (bf16_t)lo, b = (bf16_t)hi;
-  return (uint32_t)__builtin_bit_cast(uint16_t, a) |
-         ((uint32_t)__builtin_bit_cast(uint16_t, b) << 16);
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  typedef bf16_t bf16x2 __attribute__((ext_vector_type(2)));
+  const f32x2 v = {lo, hi};
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
 }
 
 template <bool FULL>
@@ -119,6 +121,17 @@ __device__ __forceinline__ void store8(float* __restrict__ row, int c, int H, co
   }
 }
 
+// The same for a caller that knows (FULL) that [c, c + 8) lies in the row: no
+// condition remains.
+template <bool FULL, typename T>
+__device__ __forceinline__ Raw8<T> load8_in(const T* row, int c, int H) {
+  return FULL ? load8<true>(row, c, c + 8) : load8<false>(row, c, H);
+}
+template <bool FULL, typename T>
+__device__ __forceinline__ void store8_in(T* row, int c, int H, const float v[8]) {
+  FULL ? store8<true>(row, c, c + 8, v) : store8<false>(row, c, H, v);
+}
+
 // ---- reductions over lanes -----------------------------------------------
 // Data-parallel-primitive controls: lane ^ 1 and lane ^ 2 within a quad, and
 // the mirrors within 8 and within 16 lanes.  After the first two every quad
@@ -139,13 +152,18 @@ __device__ __forceinline__ float row16_sum(float x) {
   x += dpp<kMirror16>(x);
   return x;
 }
-// Largest value over each 16 lanes (no NaN among them).
-__device__ __forceinline__ float row16_max(float x) {
-  x = fmaxf(x, dpp<kXor1>(x));
-  x = fmaxf(x, dpp<kXor2>(x));
-  x = fmaxf(x, dpp<kMirror8>(x));
-  x = fmaxf(x, dpp<kMirror16>(x));
-  return x;
+// Largest value over each 16 (LANES = 8: each 8) lanes.
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp_max(uint32_t x) {
+  const uint32_t y = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, CTRL, 0xF, 0xF, true);
+  return x > y ? x : y;
+}
+template <int LANES>
+__device__ __forceinline__ uint32_t lanes_max(uint32_t x) {
+  x = dpp_max<kXor1>(x);
+  x = dpp_max<kXor2>(x);
+  x = dpp_max<kMirror8>(x);
+  return LANES == 8 ? x : dpp_max<kMirror16>(x);
 }
 // Sum over the wave (every lane must be active), the same on all lanes.
 __device__ __forceinline__ float wave_sum(float x) {
@@ -156,6 +174,21 @@ __device__ __forceinline__ float wave_sum(float x) {
   const float d = __builtin_bit_cast(float, __builtin_amdgcn_readlane(r, 48));
   return (a + b) + (c + d);
 }
+
+// The value that lane `from` (the same on all lanes) holds.
+__device__ __forceinline__ float lane_value(float x, int from) {
+  return __builtin_bit_cast(float,
+                            __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), from));
+}
+
+// A use of x that computes nothing: a load into it has come by then.
+template <typename X>
+__device__ __forceinline__ void arrived(X& x) {
+  asm volatile("" : "+v"(x));
+}
+
+__device__ __forceinline__ void arrived(Raw8<bf16_t>& r) { arrived(r.w[0]); }
+__device__ __forceinline__ void arrived(Raw8<float>& r) { arrived(r.w[0]), arrived(r.w[4]); }
 
 // ---- 8-bit checkpoint ------------------------------------------------------
 // A block of 128 entries x is kept as e4m3 values q and one byte b for the
@@ -168,11 +201,11 @@ __device__ __forceinline__ float wave_sum(float x) {
 // and leaves its neighbours as they are.
 constexpr int kCkptBlock = 128;
 
-// The block's byte from its largest finite magnitude: 448 = 1.75 * 2^8, so
-// e = (exponent of top) - 8, one more when top's significand passes 1.75.
-__device__ __forceinline__ uint32_t ckpt_exp_byte(float top) {
-  const uint32_t u = __float_as_uint(top);
-  const int b = (int)(u >> 23) - 8 + ((u & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+// The block's byte from the bits of its largest finite magnitude:
+// 448 = 1.75 * 2^8, so e = (exponent of top) - 8, one more when top's
+// significand passes 1.75.
+__device__ __forceinline__ uint32_t ckpt_exp_byte(uint32_t top) {
+  const int b = (int)(top >> 23) - 8 + ((top & 0x7FFFFFu) > 0x600000u ? 1 : 0);
   return (uint32_t)(b > 0 ? b : 0);
 }
 __device__ __forceinline__ float ckpt_inv_scale(uint32_t b) {  // 2^-e, b <= 247
@@ -182,12 +215,44 @@ __device__ __forceinline__ float ckpt_scale(uint32_t b) {  // 2^e; 2^-127 is sub
   return __uint_as_float(b ? b << 23 : 0x00400000u);
 }
 
-// Codes of eight entries, given 2^-e.
+// Largest magnitude of eight entries, as fp32 bits; an infinity or NaN gives
+// kNonFinite or more.
+constexpr uint32_t kNonFinite = 0x7F800000u;
+__device__ __forceinline__ uint32_t top8(const Raw8<bf16_t>& r) {
+  typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+  u16x2 m = __builtin_bit_cast(u16x2, r.w[0] & 0x7FFF7FFFu);
+#pragma unroll
+  for (int i = 1; i < 4; ++i)
+    m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, r.w[i] & 0x7FFF7FFFu));
+  return (uint32_t)(m.x > m.y ? m.x : m.y) << 16;
+}
+__device__ __forceinline__ uint32_t top8(const Raw8<float>& r) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t a = __float_as_uint(r.w[i]) & 0x7FFFFFFFu;
+    m = m > a ? m : a;
+  }
+  return m;
+}
+// The same over the finite ones alone.
+__device__ __forceinline__ uint32_t finite_top8(const float v[8]) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t a = __float_as_uint(v[i]) & 0x7FFFFFFFu;
+    m = a < kNonFinite && a > m ? a : m;
+  }
+  return m;
+}
+
+// Codes of eight entries, given 2^-e.  CHECK: some may not be finite.
+template <bool CHECK>
 __device__ __forceinline__ uint2 ckpt_encode8(const float v[8], float inv) {
   float s[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i)
-    s[i] = __builtin_isfinite(v[i]) ? v[i] * inv : __builtin_nanf("");
+    s[i] = !CHECK || __builtin_isfinite(v[i]) ? v[i] * inv : __builtin_nanf("");
   int lo = 0, hi = 0;
   lo = __builtin_amdgcn_cvt_pk_fp8_f32(s[0], s[1], lo, false);
   lo = __builtin_amdgcn_cvt_pk_fp8_f32(s[2], s[3], lo, true);
@@ -205,17 +270,6 @@ __device__ __forceinline__ void ckpt_decode8(uint2 q, float scale, float v[8]) {
   const f32x2 d = __builtin_amdgcn_cvt_pk_f32_fp8((int)q.y, true);
   v[0] = a.x * scale, v[1] = a.y * scale, v[2] = b.x * scale, v[3] = b.y * scale;
   v[4] = c.x * scale, v[5] = c.y * scale, v[6] = d.x * scale, v[7] = d.y * scale;
-}
-
-// Largest finite magnitude of eight entries (0 if none).
-__device__ __forceinline__ float finite_top8(const float v[8]) {
-  float m = 0.f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float a = fabsf(v[i]);
-    m = fmaxf(m, a < __builtin_inff() ? a : 0.f);
-  }
-  return m;
 }
 
 template <bool FULL>
@@ -240,6 +294,11 @@ __device__ __forceinline__ uint2 load8_codes(const uint8_t* __restrict__ row, in
 }
 
 template <bool FULL>
+__device__ __forceinline__ uint2 load8_codes_in(const uint8_t* row, int c, int H) {
+  return FULL ? load8_codes<true>(row, c, c + 8) : load8_codes<false>(row, c, H);
+}
+
+template <bool FULL>
 __device__ __forceinline__ void store8_codes(uint8_t* __restrict__ row, int c, int H, uint2 q) {
   if (c + 8 <= H) {
     u32x2_a1 v;
@@ -249,6 +308,25 @@ __device__ __forceinline__ void store8_codes(uint8_t* __restrict__ row, int c, i
 #pragma unroll
     for (int i = 0; i < 7; ++i)
       if (c + i < H) row[c + i] = (uint8_t)((i < 4 ? q.x : q.y) >> (8 * (i & 3)));
+  }
+}
+
+template <bool FULL>
+__device__ __forceinline__ void store8_codes_in(uint8_t* row, int c, int H, uint2 q) {
+  FULL ? store8_codes<true>(row, c, c + 8, q) : store8_codes<false>(row, c, H, q);
+}
+
+// Sixteen codes at once where the row has them all (a 16-byte access).
+template <bool FULL>
+__device__ __forceinline__ void store16_codes(uint8_t* __restrict__ row, int c, int H, uint2 q0,
+                                              uint2 q1) {
+  if (FULL || c + 16 <= H) {
+    u32x4_a1 v;
+    v.x = q0.x, v.y = q0.y, v.z = q1.x, v.w = q1.y;
+    *reinterpret_cast<u32x4_a1*>(row + c) = v;
+  } else {
+    store8_codes<false>(row, c, H, q0);
+    store8_codes<false>(row, c + 8, H, q1);
   }
 }
 
