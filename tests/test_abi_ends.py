@@ -197,8 +197,8 @@ def test_binding_refuses_wrong_types_and_shapes():
     with pytest.raises(ValueError, match="device tensor"):
         B.mdlm_embed(ids, m(8, 16), 1.0, m(3, 16))
     with pytest.raises(TypeError, match="float32"):
-        B._shaped(m(8, 16), (8, 16), torch.float32, "d_table")
+        B._arg(m(8, 16), "d_table", torch.float32, (8, 16), -1)
     with pytest.raises(ValueError, match="shape"):
-        B._ckpt8_shapes(m(3, 130, dtype=torch.uint8), m(3, 1, dtype=torch.uint8), (3, 130))
+        B._ckpt8_args(m(3, 130, dtype=torch.uint8), m(3, 1, dtype=torch.uint8), (3, 130), -1)
     with pytest.raises(TypeError, match="unsupported element type"):
         B.dtype_code(m(2, dtype=torch.float16))

@@ -9,6 +9,7 @@ implementation.
 """
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -457,74 +458,73 @@ def mdlm_scale(x, y, scale, stream=None):
     _check(load().mdlm_scale(_ptr(x), _ptr(y), dt, x.numel(), _ptr(scale), _stream(stream)))
 
 
-def _same_device(dev, **tensors):
-    """Contiguous device tensors of the call, all on `dev`."""
-    for name, t in tensors.items():
-        if t is None:
-            continue
-        if t.device != dev:
-            raise ValueError(f"{name}: expected a tensor on {dev}, got {t.device}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name}: expected a contiguous tensor")
+# The calls below are made many times a step on small tensors, so their checks
+# are one pass over each argument, and the stream is read as the plain handle.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _place(t, name):
+    """The device index of the tensor that a call's others must share."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name}: expected a device tensor")
+    return dev
+
+
+def _arg(t, name, dtype, shape, dev):
+    """The address of a contiguous tensor of this type, shape and device (None
+    of None)."""
+    if t is None:
+        return None
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: expected a tensor on device {dev}, got {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous tensor")
+    return t.data_ptr()
 
 
 def _rows(x, name):
-    """(n, H) of a tensor [..., H] taken as rows, and its element type code."""
-    if not x.is_cuda:
-        raise ValueError(f"{name}: expected a device tensor")
+    """(n, H) of a tensor [..., H] taken as rows."""
     if x.dim() == 0:
         raise ValueError(f"{name}: expected [..., H]")
     H = x.shape[-1]
-    return (x.numel() // H if H else 0), H, dtype_code(x)
+    return (x.numel() // H if H else 0), H
 
 
-def _shaped(t, shape, dtype, name):
-    if t is None:
-        return
-    if t.dtype != dtype:
-        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+def _launch(fn, dev, stream, *args):
+    """Calls `fn` with `args` and the stream (torch's current one of the
+    device unless one is given), the device being the current one meanwhile."""
+    if stream is None:
+        handle = _raw_stream(dev)
+    elif stream.device.index != dev:
+        raise ValueError(f"stream: expected a stream of device {dev}, got one of {stream.device}")
+    else:
+        handle = stream.cuda_stream
+    if dev == torch.cuda.current_device():
+        code = fn(*args, handle)
+    else:
+        with torch.cuda.device(dev):
+            code = fn(*args, handle)
+    if code != MDLM_OK:
+        _check(code)
 
 
-def _at(t):
-    return None if t is None else t.data_ptr()
-
-
-class _On:
-    """The tensors' device as the current one, and the stream to launch on
-    (torch's current stream of that device unless one is given)."""
-
-    def __init__(self, dev, stream):
-        self.stream = stream  # None: the current one
-        if stream is None:
-            stream = torch.cuda.current_stream(dev)
-        elif stream.device != dev:
-            raise ValueError(f"stream: expected a stream of {dev}, got one of {stream.device}")
-        self.handle = stream.cuda_stream
-        self.guard = torch.cuda.device(dev) if dev.index != torch.cuda.current_device() else None
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-        return self
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
-
-    def scratch(self, dev, nbytes, workspace):
-        """(address, bytes, owner) of the caller's workspace, or of one allocated
-        on the launch stream for this call."""
-        if workspace is None and nbytes > 0:
-            with torch.cuda.stream(self.stream):
-                workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-        if workspace is None:
-            return None, 0, None
-        if workspace.dtype != torch.uint8:
-            raise TypeError(f"workspace: expected torch.uint8, got {workspace.dtype}")
-        _same_device(dev, workspace=workspace)
-        return workspace.data_ptr(), workspace.numel(), workspace
+def _scratch(workspace, nbytes, dev, stream):
+    """The caller's workspace, or one allocated for the call on the stream it
+    will run on; None if none is needed."""
+    if workspace is not None:
+        _arg(workspace, "workspace", torch.uint8, (workspace.numel(),), dev)
+        return workspace
+    if nbytes == 0:
+        return None
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
 
 
 def mdlm_embed(ids, table, scale, out, stream=None):
@@ -534,17 +534,14 @@ def mdlm_embed(ids, table, scale, out, stream=None):
     if table.dim() != 2:
         raise ValueError("table: expected [V, H]")
     V, H = table.shape
-    _, _, dt = _rows(table, "table")
-    dev = table.device
-    if ids.dtype != torch.int32:
-        raise TypeError(f"ids: expected torch.int32, got {ids.dtype}")
-    _shaped(out, (*ids.shape, H), table.dtype, "out")
-    _same_device(dev, ids=ids, table=table, out=out)
-    with _On(dev, stream) as on:
-        _check(load().mdlm_embed(ids.data_ptr(), ids.numel(), table.data_ptr(), dt, V, H,
-                                 float(scale), out.data_ptr(), on.handle))
+    dt = dtype_code(table)
+    dev = _place(table, "table")
+    _launch(load().mdlm_embed, dev, stream, _arg(ids, "ids", torch.int32, ids.shape, dev),
+            ids.numel(), _arg(table, "table", table.dtype, table.shape, dev), dt, V, H, float(scale),
+            _arg(out, "out", table.dtype, (*ids.shape, H), dev))
 
 
+@functools.lru_cache(maxsize=256)
 def mdlm_embed_grad_workspace_bytes(n_tokens, H):
     return load().mdlm_embed_grad_workspace_bytes(int(n_tokens), int(H))
 
@@ -556,24 +553,22 @@ def mdlm_embed_grad(ids, d_out, scale, d_table, accumulate=False, workspace=None
     if d_table.dim() != 2:
         raise ValueError("d_table: expected [V, H]")
     V, H = d_table.shape
-    if ids.dtype != torch.int32:
-        raise TypeError(f"ids: expected torch.int32, got {ids.dtype}")
-    n, _, dt = _rows(d_out, "d_out")
-    dev = d_out.device
-    _shaped(d_out, (*ids.shape, H), d_out.dtype, "d_out")
-    _shaped(d_table, (V, H), torch.float32, "d_table")
-    _same_device(dev, ids=ids, d_out=d_out, d_table=d_table)
-    lib = load()
-    with _On(dev, stream) as on:
-        ws, ws_bytes, _keep = on.scratch(dev, lib.mdlm_embed_grad_workspace_bytes(n, H), workspace)
-        _check(lib.mdlm_embed_grad(ids.data_ptr(), n, d_out.data_ptr(), dt, V, H, float(scale),
-                                   d_table.data_ptr(), 1 if accumulate else 0, ws, ws_bytes,
-                                   on.handle))
+    n = ids.numel()
+    dt = dtype_code(d_out)
+    dev = _place(d_out, "d_out")
+    a_ids = _arg(ids, "ids", torch.int32, ids.shape, dev)
+    a_out = _arg(d_out, "d_out", d_out.dtype, (*ids.shape, H), dev)
+    a_table = _arg(d_table, "d_table", torch.float32, d_table.shape, dev)
+    ws = _scratch(workspace, mdlm_embed_grad_workspace_bytes(n, H), dev, stream)
+    _launch(load().mdlm_embed_grad, dev, stream, a_ids, n, a_out, dt, V, H, float(scale), a_table,
+            1 if accumulate else 0, None if ws is None else ws.data_ptr(),
+            0 if ws is None else ws.numel())
 
 
-def _ckpt8_shapes(q, q_exp, shape):
-    _shaped(q, shape, torch.uint8, "q")
-    _shaped(q_exp, (*shape[:-1], -(-shape[-1] // MDLM_CKPT8_BLOCK)), torch.uint8, "q_exp")
+def _ckpt8_args(q, q_exp, shape, dev):
+    return (_arg(q, "q", torch.uint8, shape, dev),
+            _arg(q_exp, "q_exp", torch.uint8,
+                 (*shape[:-1], -(-shape[-1] // MDLM_CKPT8_BLOCK)), dev))
 
 
 def mdlm_norm_fwd(x, kind, weight, bias, eps, y, mean=None, rstd=None, q=None, q_exp=None,
@@ -581,46 +576,36 @@ def mdlm_norm_fwd(x, kind, weight, bias, eps, y, mean=None, rstd=None, q=None, q
     """See mdlm_norm_fwd in include/mdlm.h: `x`, `y` [..., H], `weight` and
     `bias` [H] of x's type or None, `mean` and `rstd` float32 [...] or None,
     `q` [..., H] and `q_exp` [..., ceil(H / 128)] uint8 or both None."""
-    n, H, dt = _rows(x, "x")
-    dev, lead = x.device, x.shape[:-1]
-    _shaped(weight, (H,), x.dtype, "weight")
-    _shaped(bias, (H,), x.dtype, "bias")
-    _shaped(y, x.shape, x.dtype, "y")
-    _shaped(mean, lead, torch.float32, "mean")
-    _shaped(rstd, lead, torch.float32, "rstd")
-    _ckpt8_shapes(q, q_exp, x.shape)
-    _same_device(dev, x=x, weight=weight, bias=bias, y=y, mean=mean, rstd=rstd, q=q, q_exp=q_exp)
-    with _On(dev, stream) as on:
-        _check(load().mdlm_norm_fwd(x.data_ptr(), dt, n, H, int(kind), _at(weight), _at(bias),
-                                    float(eps), y.data_ptr(), _at(mean), _at(rstd), _at(q),
-                                    _at(q_exp), on.handle))
+    n, H = _rows(x, "x")
+    T, shape, lead = x.dtype, x.shape, x.shape[:-1]
+    dt = dtype_code(x)
+    dev = _place(x, "x")
+    a_q, a_exp = _ckpt8_args(q, q_exp, shape, dev)
+    _launch(load().mdlm_norm_fwd, dev, stream, _arg(x, "x", T, shape, dev), dt, n, H, int(kind),
+            _arg(weight, "weight", T, (H,), dev), _arg(bias, "bias", T, (H,), dev), float(eps),
+            _arg(y, "y", T, shape, dev), _arg(mean, "mean", torch.float32, lead, dev),
+            _arg(rstd, "rstd", torch.float32, lead, dev), a_q, a_exp)
 
 
+@functools.lru_cache(maxsize=256)
 def mdlm_norm_bwd_workspace_bytes(n, H):
     return load().mdlm_norm_bwd_workspace_bytes(int(n), int(H))
 
 
-def _norm_bwd(name, dy, source, kind, weight, mean, rstd, dx, d_weight, d_bias, accumulate,
-              workspace, stream):
-    n, H, dt = _rows(dy, "dy")
-    dev, lead = dy.device, dy.shape[:-1]
-    _shaped(weight, (H,), dy.dtype, "weight")
-    _shaped(mean, lead, torch.float32, "mean")
-    _shaped(rstd, lead, torch.float32, "rstd")
-    _shaped(dx, dy.shape, dy.dtype, "dx")
-    _shaped(d_weight, (H,), torch.float32, "d_weight")
-    _shaped(d_bias, (H,), torch.float32, "d_bias")
-    _same_device(dev, dy=dy, weight=weight, mean=mean, rstd=rstd, dx=dx, d_weight=d_weight,
-                 d_bias=d_bias, **source)
-    lib = load()
-    need = (lib.mdlm_norm_bwd_workspace_bytes(n, H)
+def _norm_bwd(fn, dy, source, kind, weight, mean, rstd, dx, d_weight, d_bias, accumulate,
+              workspace, stream, dev):
+    n, H = _rows(dy, "dy")
+    T, lead, f32 = dy.dtype, dy.shape[:-1], torch.float32
+    args = (_arg(dy, "dy", T, dy.shape, dev), *source, dtype_code(dy), n, H, int(kind),
+            _arg(weight, "weight", T, (H,), dev), _arg(mean, "mean", f32, lead, dev),
+            _arg(rstd, "rstd", f32, lead, dev), _arg(dx, "dx", T, dy.shape, dev),
+            _arg(d_weight, "d_weight", f32, (H,), dev), _arg(d_bias, "d_bias", f32, (H,), dev),
+            1 if accumulate else 0)
+    need = (mdlm_norm_bwd_workspace_bytes(n, H)
             if d_weight is not None or d_bias is not None else 0)
-    with _On(dev, stream) as on:
-        ws, ws_bytes, _keep = on.scratch(dev, need, workspace)
-        _check(getattr(lib, name)(dy.data_ptr(), *[_at(t) for t in source.values()], dt, n, H,
-                                  int(kind), _at(weight), _at(mean), _at(rstd), _at(dx),
-                                  _at(d_weight), _at(d_bias), 1 if accumulate else 0, ws,
-                                  ws_bytes, on.handle))
+    ws = _scratch(workspace, need, dev, stream)
+    _launch(fn, dev, stream, *args, None if ws is None else ws.data_ptr(),
+            0 if ws is None else ws.numel())
 
 
 def mdlm_norm_bwd(dy, x, kind, weight, mean, rstd, dx, d_weight=None, d_bias=None,
@@ -629,39 +614,37 @@ def mdlm_norm_bwd(dy, x, kind, weight, mean, rstd, dx, d_weight=None, d_bias=Non
     `mean` (None for RMS) and `rstd` as mdlm_norm_fwd left them, `d_weight` and
     `d_bias` float32 [H]; outputs not wanted are None; `workspace` a uint8
     tensor, allocated for the call if None."""
-    _shaped(x, dy.shape, dy.dtype, "x")
-    _norm_bwd("mdlm_norm_bwd", dy, {"x": x}, kind, weight, mean, rstd, dx, d_weight, d_bias,
-              accumulate, workspace, stream)
+    dev = _place(dy, "dy")
+    _norm_bwd(load().mdlm_norm_bwd, dy, (_arg(x, "x", dy.dtype, dy.shape, dev),), kind, weight,
+              mean, rstd, dx, d_weight, d_bias, accumulate, workspace, stream, dev)
 
 
 def mdlm_norm_bwd_ckpt8(dy, q, q_exp, kind, weight, mean, rstd, dx, d_weight=None, d_bias=None,
                         accumulate=False, workspace=None, stream=None):
     """See mdlm_norm_bwd_ckpt8 in include/mdlm.h: mdlm_norm_bwd with x as the
     8-bit checkpoint `q`, `q_exp` holds it."""
-    _ckpt8_shapes(q, q_exp, dy.shape)
-    _norm_bwd("mdlm_norm_bwd_ckpt8", dy, {"q": q, "q_exp": q_exp}, kind, weight, mean, rstd, dx,
-              d_weight, d_bias, accumulate, workspace, stream)
+    dev = _place(dy, "dy")
+    _norm_bwd(load().mdlm_norm_bwd_ckpt8, dy, _ckpt8_args(q, q_exp, dy.shape, dev), kind, weight,
+              mean, rstd, dx, d_weight, d_bias, accumulate, workspace, stream, dev)
 
 
 def mdlm_ckpt8_save(x, q, q_exp, stream=None):
     """See mdlm_ckpt8_save in include/mdlm.h: `x` [..., H] bf16 or float32 into
     `q` [..., H] and `q_exp` [..., ceil(H / 128)] uint8."""
-    n, H, dt = _rows(x, "x")
-    _ckpt8_shapes(q, q_exp, x.shape)
-    _same_device(x.device, x=x, q=q, q_exp=q_exp)
-    with _On(x.device, stream) as on:
-        _check(load().mdlm_ckpt8_save(x.data_ptr(), dt, n, H, q.data_ptr(), q_exp.data_ptr(),
-                                      on.handle))
+    n, H = _rows(x, "x")
+    dt = dtype_code(x)
+    dev = _place(x, "x")
+    _launch(load().mdlm_ckpt8_save, dev, stream, _arg(x, "x", x.dtype, x.shape, dev), dt, n, H,
+            *_ckpt8_args(q, q_exp, x.shape, dev))
 
 
 def mdlm_ckpt8_load(q, q_exp, x, stream=None):
     """See mdlm_ckpt8_load in include/mdlm.h: the checkpoint restored into `x`."""
-    n, H, dt = _rows(x, "x")
-    _ckpt8_shapes(q, q_exp, x.shape)
-    _same_device(x.device, x=x, q=q, q_exp=q_exp)
-    with _On(x.device, stream) as on:
-        _check(load().mdlm_ckpt8_load(q.data_ptr(), q_exp.data_ptr(), dt, n, H, x.data_ptr(),
-                                      on.handle))
+    n, H = _rows(x, "x")
+    dt = dtype_code(x)
+    dev = _place(x, "x")
+    _launch(load().mdlm_ckpt8_load, dev, stream, *_ckpt8_args(q, q_exp, x.shape, dev), dt, n, H,
+            _arg(x, "x", x.dtype, x.shape, dev))
 
 
 def mdlm_check_offsets(cu_seqlens, n_tokens, status, stream=None):

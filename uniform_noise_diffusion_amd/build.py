@@ -10,6 +10,8 @@ import os
 import shutil
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG_DIR)
@@ -23,7 +25,7 @@ PROBE_SOURCES = ["probe.hip"]
 ARCH = os.environ.get("MDLM_OFFLOAD_ARCH", "gfx950")
 
 HIPCC_FLAGS = [
-    "-O3", "-std=c++17", "-fPIC", "-shared",
+    "-O3", "-std=c++17", "-fPIC",
     f"--offload-arch={ARCH}",
     # no packed fp32 instructions in device code
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
@@ -38,10 +40,7 @@ def hipcc():
     return path
 
 
-def _compile(sources, out, verbose):
-    srcs = [os.path.join(CSRC, s) for s in sources]
-    tmp = out + ".tmp"
-    cmd = [hipcc(), *HIPCC_FLAGS, "-I", INCLUDE, "-I", CSRC, *srcs, "-o", tmp]
+def _run(cmd, verbose):
     if verbose:
         print(" ".join(cmd), flush=True)
     res = subprocess.run(cmd, capture_output=True, text=True)
@@ -51,7 +50,22 @@ def _compile(sources, out, verbose):
         raise RuntimeError(f"hipcc failed ({res.returncode}):\n{err}")
     if verbose and err.strip():
         print(err, file=sys.stderr)
-    os.replace(tmp, out)
+
+
+def _compile(sources, out, verbose):
+    """One object per source, side by side (no device code crosses a source),
+    then the library."""
+    with tempfile.TemporaryDirectory() as tmp:
+        def one(name):
+            obj = os.path.join(tmp, name + ".o")
+            _run([hipcc(), *HIPCC_FLAGS, "-c", "-I", INCLUDE, "-I", CSRC,
+                  os.path.join(CSRC, name), "-o", obj], verbose)
+            return obj
+
+        with ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as pool:
+            objs = list(pool.map(one, sources))
+        _run([hipcc(), "-shared", f"--offload-arch={ARCH}", *objs, "-o", out + ".tmp"], verbose)
+    os.replace(out + ".tmp", out)
     return out
 
 

@@ -69,23 +69,24 @@ __device__ __forceinline__ uint32_t sort_id(int32_t id, int32_t V) {
   return (uint32_t)id < (uint32_t)V ? (uint32_t)id : (uint32_t)V;
 }
 
-// Clears the table: one 16-byte store per thread, the blocks in order.  This
+// Clears n floats: one 16-byte store per thread, the blocks in order.  This
 // pattern writes fastest here: 305 us for the 2.07 GB of a 126,464 x 4,096
 // table (6.8 TB/s); four stores a thread took 345 us, whole rows by waves that
-// first look whether the row is written anyway 350 us, and sharing the launch
-// with the sorting (blocks of 1,024) 325 us.
-__global__ void __launch_bounds__(kThreads)
-clear_kernel(float* __restrict__ p, int64_t n) {
+// first look whether the row is written anyway 350 us.
+__device__ __forceinline__ void clear(float* __restrict__ p, int64_t n, int64_t thread,
+                                      int64_t threads) {
   // 16-byte words from the first address that is a multiple of 16
   int64_t head = (int64_t)((16 - (reinterpret_cast<uintptr_t>(p) & 15)) / 4 & 3);
   head = head < n ? head : n;
   const int64_t n4 = (n - head) / 4, tail = n - head - 4 * n4;
-  const int64_t t = (int64_t)blockIdx.x * kThreads + threadIdx.x;
   float4* words = reinterpret_cast<float4*>(p + head);
-  for (int64_t i = t; i < n4; i += (int64_t)gridDim.x * kThreads)
-    words[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (t < head) p[t] = 0.f;
-  if (t < tail) p[head + 4 * n4 + t] = 0.f;
+  for (int64_t i = thread; i < n4; i += threads) words[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (thread < head) p[thread] = 0.f;
+  if (thread < tail) p[head + 4 * n4 + thread] = 0.f;
+}
+
+__global__ void __launch_bounds__(kThreads) clear_kernel(float* __restrict__ p, int64_t n) {
+  clear(p, n, (int64_t)blockIdx.x * kThreads + threadIdx.x, (int64_t)gridDim.x * kThreads);
 }
 
 // Of four ids in LDS, the number below `key`.
@@ -105,7 +106,13 @@ __device__ __forceinline__ int count_below(const uint32_t* s_id, int q, uint32_t
 // and 19 us.)
 __global__ void __launch_bounds__(kRankThreads)
 rank_kernel(const int32_t* __restrict__ ids, int64_t n, int64_t len, int32_t V,
-            int32_t* __restrict__ sid, int32_t* __restrict__ spos, int64_t per_block) {
+            int32_t* __restrict__ sid, int32_t* __restrict__ spos, int64_t per_block,
+            int32_t rank_blocks, float* __restrict__ fill, int64_t fill_n) {
+  if ((int)blockIdx.x >= rank_blocks) {
+    clear(fill, fill_n, (int64_t)(blockIdx.x - rank_blocks) * kRankThreads + threadIdx.x,
+          (int64_t)(gridDim.x - rank_blocks) * kRankThreads);
+    return;
+  }
   __shared__ __align__(16) uint32_t s_id[kOneRun];
   __shared__ int s_count[kRankWaves][kRankI];
   const int tid = threadIdx.x, lane = tid & 63;
@@ -532,7 +539,11 @@ join_runs_kernel(const int32_t* __restrict__ sid, int64_t n, int32_t V, int32_t 
 
 int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 
-// Entries of the sorted list per chunk.
+// Floats of a table that the sorting launch clears.
+constexpr int64_t kSmallTable = (int64_t)16 << 20;
+
+// Entries of the sorted list per chunk: the most, up to 32, that leave 2,048
+// waves (two per SIMD) something to do, and four at the least.
 int chunk_of(int64_t n, int32_t H) {
   const int64_t slabs = (H + 511) / 512;
   int C = kMaxChunk;
@@ -607,19 +618,22 @@ hipError_t launch_embed_grad(const int32_t* ids, int64_t n, const void* d_out, i
   const int C = chunk_of(n, H);
   uint8_t* cut = reinterpret_cast<uint8_t*>(ws + 4 * list);
   float* part = reinterpret_cast<float*>(ws + 4 * list + round_up((n + C - 1) / C, 256));
-  if (!accumulate) {
-    const int64_t words = (int64_t)V * H / 4;
-    clear_kernel<<<(unsigned)std::min<int64_t>(words / kThreads + 1, (int64_t)1 << 23), kThreads,
-                   0, stream>>>(d_table, (int64_t)V * H);
-  }
+  const int64_t table_n = (int64_t)V * H;
+  const bool apart = n == 0 || table_n > kSmallTable;
+  if (!accumulate && apart)
+    clear_kernel<<<(unsigned)std::min<int64_t>(table_n / 4 / kThreads + 1, (int64_t)1 << 23),
+                   kThreads, 0, stream>>>(d_table, table_n);
   if (n == 0) return hipGetLastError();
   // Neighbouring tokens share a block where there are more than two blocks per
   // compute unit: they share the ids in LDS.
   const int64_t len = n <= kOneRun ? n : kRun;
   const int64_t groups = (n + len - 1) / len * ((len + kRankI - 1) / kRankI);
   const int64_t per_rank = (groups + 511) / 512;
-  rank_kernel<<<(unsigned)((groups + per_rank - 1) / per_rank), kRankThreads, 0, stream>>>(
-      ids, n, len, V, sid[0], spos[0], per_rank);
+  const int64_t ranks = (groups + per_rank - 1) / per_rank;
+  const int64_t fill_n = accumulate || apart ? 0 : table_n;
+  const int64_t fills = fill_n > 0 ? fill_n / 4 / kRankThreads + 1 : 0;
+  rank_kernel<<<(unsigned)(ranks + fills), kRankThreads, 0, stream>>>(
+      ids, n, len, V, sid[0], spos[0], per_rank, (int32_t)ranks, d_table, fill_n);
   int from = 0;
   if (n > kOneRun) {
     const int64_t sets = (n + 63) / 64, per_merge = (sets + 255) / 256;
