@@ -202,3 +202,41 @@ def test_binding_refuses_wrong_types_and_shapes():
         B._ckpt8_args(m(3, 130, dtype=torch.uint8), m(3, 1, dtype=torch.uint8), (3, 130), -1)
     with pytest.raises(TypeError, match="unsupported element type"):
         B.dtype_code(m(2, dtype=torch.float16))
+
+
+def test_launch_makes_the_tensors_device_current(monkeypatch):
+    """The library launches on the current device: a call on another device's
+    tensors switches to it, and back."""
+    seen, now = [], [0]
+
+    class Device:
+        def __init__(self, index):
+            self.index = index
+
+        def __enter__(self):
+            self.was, now[0] = now[0], self.index
+
+        def __exit__(self, *exc):
+            now[0] = self.was
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: now[0])
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setattr(B, "_raw_stream", lambda dev: 1000 + dev)
+
+    def fn(*args):
+        seen.append((now[0], args))
+        return B.MDLM_OK
+
+    B._launch(fn, 0, None, "a")
+    B._launch(fn, 3, None, "b")
+    assert seen == [(0, ("a", 1000)), (3, ("b", 1003))] and now[0] == 0
+
+    class Stream:
+        device = torch.device("cuda", 2)
+        cuda_stream = 77
+
+    B._launch(fn, 2, Stream, "c")
+    assert seen[-1] == (2, ("c", 77))
+    with pytest.raises(ValueError, match="stream"):
+        B._launch(fn, 1, Stream, "d")
+    assert len(seen) == 3

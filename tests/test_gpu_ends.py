@@ -288,3 +288,63 @@ def test_chain_of_differentiable_calls():
     assert abs(float(loss) - float(l64)) < 1e-3 * abs(float(l64))
     err = (T.grad.double().cpu() - T64.grad).norm() / T64.grad.norm()
     assert float(err) < 1e-2
+
+
+def test_each_call_captured_with_its_own_workspace():
+    """Every call by itself in one graph, workspaces allocated inside the
+    capture; replays on new inputs, with eager calls between, against eager
+    results bit for bit."""
+    n, H, V = 700, 200, 300
+    g = torch.Generator(device=DEV).manual_seed(9)
+    ids = torch.randint(-1, V, (n,), device=DEV, generator=g, dtype=torch.int32)
+    x, dy = (torch.randn(n, H, device=DEV, generator=g).bfloat16() for _ in range(2))
+    T = torch.randn(V, H, device=DEV, generator=g).bfloat16()
+    w = torch.randn(H, device=DEV, generator=g).bfloat16()
+
+    def go():
+        f32 = dict(device=DEV, dtype=torch.float32)
+        emb, y, back, dx = (torch.empty(n, H, device=DEV, dtype=torch.bfloat16)
+                            for _ in range(4))
+        d_t, dw, db = torch.empty(V, H, **f32), torch.empty(H, **f32), torch.empty(H, **f32)
+        mean, rstd = torch.empty(n, **f32), torch.empty(n, **f32)
+        q = torch.empty(n, H, device=DEV, dtype=torch.uint8)
+        qe = torch.empty(n, 2, device=DEV, dtype=torch.uint8)
+        B.mdlm_embed(ids, T, 0.5, emb)
+        B.mdlm_norm_fwd(x, B.MDLM_NORM_LAYER, w, None, 1e-6, y, mean, rstd)
+        B.mdlm_norm_bwd(dy, x, B.MDLM_NORM_LAYER, w, mean, rstd, dx, dw, db)
+        B.mdlm_embed_grad(ids, dy, 0.5, d_t)
+        B.mdlm_ckpt8_save(x, q, qe)
+        B.mdlm_ckpt8_load(q, qe, back)
+        return emb, y, mean, rstd, dx, dw, db, d_t, back
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        go()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = go()
+    for rep in range(4):
+        x.copy_((torch.randn(n, H, device=DEV, generator=g) * (rep + 1)).bfloat16())
+        dy.copy_(torch.randn(n, H, device=DEV, generator=g).bfloat16())
+        ids.copy_(torch.randint(-1, V, (n,), device=DEV, generator=g, dtype=torch.int32))
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got, go()):
+            assert torch.equal(a, b), rep
+
+
+def test_step_without_tokens():
+    step = M.MdlmTrainStep(0, 0, 64, 90, device=DEV)
+    T = torch.randn(90, 64, device=DEV).bfloat16()
+    w = torch.ones(64, device=DEV, dtype=torch.bfloat16)
+    cu, x0 = torch.zeros(1, dtype=torch.int32, device=DEV), torch.empty(0, dtype=torch.int32,
+                                                                        device=DEV)
+    step.corrupt(x0, cu, 1, 0.3, 0, 89, 90)
+    step.compact(x0, cu, 0)
+    step.final_norm(step.embed(T), w)
+    step.head_ce_dw(T)
+    step.embed_grad(step.norm_grad())
+    assert float(step.loss) == 0.0 and not step.dW.any() and not step.d_norm_weight.any()

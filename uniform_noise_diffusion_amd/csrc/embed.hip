@@ -434,8 +434,9 @@ constexpr int kJoinThreads = 1024;
 constexpr int kJoinWaves = kJoinThreads / 64;
 
 // First of the numbers from `seen` on that is `mine` modulo `of`, from `seen`.
-__device__ __forceinline__ int first_turn(int64_t seen, int mine, int of) {
-  return (int)((mine + of - seen % of) % of);
+__device__ __forceinline__ int first_turn(uint32_t seen, uint32_t mine, uint32_t of) {
+  const uint32_t at = seen % of;  // (mine < of)
+  return (int)(mine >= at ? mine - at : mine + of - at);
 }
 
 template <bool ACC>
@@ -449,7 +450,7 @@ join_runs_kernel(const int32_t* __restrict__ sid, int64_t n, int32_t V, int32_t 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int64_t chunks = (n + C - 1) / C;
-  int64_t seen_short = 0, seen_long = 0;  // runs found before this round
+  uint32_t seen_short = 0, seen_long = 0;  // runs found before this round
   for (int64_t base = 0; base < chunks; base += kJoinThreads) {
     const int64_t m = base + tid;
     const int kind = m < chunks ? cut[m] : kNotCut;
