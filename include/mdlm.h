@@ -580,7 +580,8 @@ enum { MDLM_NORM_LAYER = 0, MDLM_NORM_RMS = 1 };
  *   RMS:   mean = 0,           rstd = 1 / sqrt(mean(x_row^2) + eps)
  *   y = (x - mean) * rstd * weight + bias
  *
- * in fp32 throughout, y rounded once to `dtype`.
+ * in fp32 throughout, y rounded once to `dtype` (entries beyond 1e19, whose
+ * squares overflow, make a variance of infinity).
  *
  *   x           [n, H] row-major, element type `dtype`.
  *   dtype       MDLM_BF16 or MDLM_F32.

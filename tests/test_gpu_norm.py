@@ -106,7 +106,8 @@ def test_norm_backward(dtype, kind, n, H):
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("n,H", [(1, 1), (3, 130), (5, 512), (9, 1001), (4, 2816), (3, 4096),
-                                 (2, 8195), (2, 16384), (700, 136)])
+                                 (5, 1000), (3, 5128), (2, 8195), (2, 8200), (2, 16384),
+                                 (700, 136)])
 def test_norm_with_checkpoint(dtype, kind, n, H):
     """The forward's checkpoint is mdlm_ckpt8_save's, bit for bit, its y that of
     the call without one; the gradients are those at the restored x."""
