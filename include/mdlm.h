@@ -556,6 +556,8 @@ int mdlm_embed(const int32_t* ids, int64_t n_tokens, const void* table, int32_t 
  *               micro-batches).
  *   workspace   >= mdlm_embed_grad_workspace_bytes(n_tokens, H) bytes of
  *               device memory, 256-byte aligned; contents on entry ignored.
+ *               (Up to 1,024 tokens with up to 2^20 entries of d_out in all
+ *               need none: 0 bytes.)
  * Calls sharing a workspace must not overlap.
  * Returns MDLM_OK, MDLM_EINVAL, MDLM_EUNSUPPORTED, MDLM_EWORKSPACE or MDLM_EHIP.
  */

@@ -72,8 +72,8 @@ def test_embed_refuses(lib, kw, code, msg):
      "256-byte"),
 ])
 def test_embed_grad_refuses(lib, kw, code, msg):
-    base = dict(ids=NULL, n=4, g=NULL, dt=1, V=8, H=64, scale=1.0, d=NULL, acc=0, ws=NULL, wsb=0,
-                st=NULL)
+    base = dict(ids=NULL, n=4000, g=NULL, dt=1, V=8, H=64, scale=1.0, d=NULL, acc=0, ws=NULL,
+                wsb=0, st=NULL)
     assert call(lib.mdlm_embed_grad, GRAD, base, kw) == code
     assert msg in B.mdlm_last_error()
 
@@ -156,7 +156,8 @@ def test_workspace_sizes(lib):
     assert B.mdlm_embed_grad_workspace_bytes(-1, 64) == 0
     assert B.mdlm_embed_grad_workspace_bytes(5, 0) == 0
     assert B.mdlm_embed_grad_workspace_bytes(1 << 31, 64) == 0
-    sizes = [B.mdlm_embed_grad_workspace_bytes(n, 100) for n in (1, 64, 5000, 1 << 20)]
+    assert B.mdlm_embed_grad_workspace_bytes(1024, 100) == 0  # few tokens need none
+    sizes = [B.mdlm_embed_grad_workspace_bytes(n, 100) for n in (1025, 1500, 5000, 1 << 20)]
     assert all(s > 0 for s in sizes) and sizes == sorted(sizes)
     assert B.mdlm_norm_bwd_workspace_bytes(0, 64) == 0
     assert B.mdlm_norm_bwd_workspace_bytes(4, 16385) == 0

@@ -136,6 +136,28 @@ def test_embed_grad_run_borders():
         check_grad(ids, len(ids), H, V, torch.float32, off % 2 == 0, 1.0, off)
 
 
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_embed_grad_of_few_tokens_and_long_rows(accumulate):
+    """Up to 1,024 tokens on both sides of the 2^20 entries up to which one
+    launch does it all, and the sorted list at its shortest."""
+    for n, H, V in ((1, 1 << 20, 3), (1, (1 << 20) + 8, 3), (3, 400_000, 2), (17, 70_000, 4),
+                    (33, 33_000, 5), (100, 10_400, 30), (255, 4112, 40), (256, 4096, 40),
+                    (257, 4096, 40), (1000, 1100, 90), (1024, 1024, 90), (1025, 1024, 90)):
+        for kind in ("absorb", "few"):
+            ids = draw_ids(np.random.default_rng(n), kind, n, V)
+            check_grad(ids, n, H, V, torch.bfloat16, accumulate, 1.25, n)
+
+
+def test_embed_grad_of_few_tokens_runs():
+    """Runs of 1 to 40 tokens, in one launch, in a table on both sides of the
+    size that the launch clears itself."""
+    for V in (41, 300_000):
+        ids = np.repeat(np.arange(41), np.arange(41)).astype(np.int32)
+        np.random.default_rng(V).shuffle(ids)
+        check_grad(ids, len(ids), 60, V, torch.float32, False, -0.5, V)
+        check_grad(ids, len(ids), 60, V, torch.float32, True, -0.5, V)
+
+
 def test_embed_grad_no_tokens():
     d = torch.full((10, 12), 7.0, device=DEV)
     ids, g = torch.empty(0, dtype=torch.int32, device=DEV), torch.empty(0, 12, device=DEV)
