@@ -688,8 +688,9 @@ few_tokens_kernel(const int32_t* __restrict__ ids, int32_t n, int32_t V, int32_t
 }
 
 // Few enough for one launch: beyond about 2^20 entries the sorted list is
-// faster (H = 4,096: 256 tokens 8 us a call against 14.6, 512 tokens 14.3
-// against 14.5, 1,024 tokens 34 against 15).
+// faster (H = 4,096, half of the tokens the mask, added to the table: 256
+// tokens 7.7 us a call against 14.3, 512 tokens 14.3 against 14.5, 1,024 tokens
+// 34 against 15).
 bool is_few(int64_t n, int32_t H) { return n <= kFewTokens && n * H <= (int64_t)1 << 20; }
 
 template <typename T, bool FULL>
