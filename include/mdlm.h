@@ -529,7 +529,7 @@ int mdlm_scale(const void* x, void* y, int32_t dtype, int64_t n, const float* sc
  *   n_tokens    >= 0, below 2^31.
  *   table       [V, H] row-major, element type `dtype`.
  *   dtype       MDLM_BF16 or MDLM_F32.
- *   V, H        > 0 (any H).
+ *   V, H        > 0, H up to 2^26.
  *   scale       finite.
  *   out         [n_tokens, H], element type `dtype`.
  * Pointers are aligned to their entries; nothing more is asked of them.

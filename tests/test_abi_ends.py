@@ -44,6 +44,8 @@ BWD8 = ("dy", "q", "qe", "dt", "n", "H", "kind", "w", "mean", "rstd", "dx", "dw"
     (dict(n=-1), B.MDLM_EINVAL, "bad sizes"),
     (dict(H=0), B.MDLM_EINVAL, "bad sizes"),
     (dict(n=1 << 31), B.MDLM_EUNSUPPORTED, "below 2^31"),
+    (dict(H=(1 << 26) + 1), B.MDLM_EUNSUPPORTED, "exceeds 67108864"),
+    (dict(H=(1 << 31) - 1), B.MDLM_EUNSUPPORTED, "exceeds 67108864"),
     (dict(V=0), B.MDLM_EINVAL, "V must"),
     (dict(scale=float("nan")), B.MDLM_EINVAL, "finite"),
     (dict(scale=float("inf")), B.MDLM_EINVAL, "finite"),
@@ -60,6 +62,8 @@ def test_embed_refuses(lib, kw, code, msg):
     (dict(dt=-1), B.MDLM_EINVAL, "dtype"),
     (dict(n=-5), B.MDLM_EINVAL, "bad sizes"),
     (dict(n=1 << 31), B.MDLM_EUNSUPPORTED, "below 2^31"),
+    (dict(H=(1 << 26) + 1), B.MDLM_EUNSUPPORTED, "exceeds 67108864"),
+    (dict(n=0, H=(1 << 31) - 1), B.MDLM_EUNSUPPORTED, "exceeds 67108864"),
     (dict(V=-2), B.MDLM_EINVAL, "V must"),
     (dict(scale=float("-inf")), B.MDLM_EINVAL, "finite"),
     (dict(acc=2), B.MDLM_EINVAL, "accumulate"),

@@ -158,6 +158,16 @@ def test_embed_grad_of_few_tokens_runs():
         check_grad(ids, len(ids), 60, V, torch.float32, True, -0.5, V)
 
 
+def test_embed_grad_of_few_tokens_into_narrow_rows():
+    """Tables on both sides of the 512 clearing blocks up to which one launch
+    also clears the table, and long ones of short rows."""
+    for H, V in ((8, 64 * 512), (8, 64 * 512 + 1), (256, 64 * 512), (256, 64 * 512 + 1),
+                 (1, 500_000), (3, 300_000)):
+        ids = draw_ids(np.random.default_rng(V), "padded", 90, V)
+        ids[:2] = 0, V - 1
+        check_grad(ids, 90, H, V, torch.float32, False, 0.75, H, skew=3 if H % 8 else 0)
+
+
 def test_embed_grad_no_tokens():
     d = torch.full((10, 12), 7.0, device=DEV)
     ids, g = torch.empty(0, dtype=torch.int32, device=DEV), torch.empty(0, 12, device=DEV)

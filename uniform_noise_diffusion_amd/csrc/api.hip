@@ -455,6 +455,7 @@ int mdlm_embed(const int32_t* ids, int64_t n_tokens, const void* table, int32_t 
   const char* fn = "mdlm_embed";
   const hipStream_t st = reinterpret_cast<hipStream_t>(stream);
   if (const int rc = check_row_sizes(fn, dtype, n_tokens, H)) return rc;
+  if (H > kEmbedMaxH) return fail(MDLM_EUNSUPPORTED, "%s: H = %d exceeds %d", fn, H, kEmbedMaxH);
   if (V <= 0) return fail(MDLM_EINVAL, "%s: V must be > 0", fn);
   if (!isfinite(scale)) return fail(MDLM_EINVAL, "%s: scale must be finite", fn);
   if (n_tokens > 0 && (!ids || !table || !out)) return fail(MDLM_EINVAL, "%s: null pointer", fn);
@@ -468,7 +469,7 @@ int mdlm_embed(const int32_t* ids, int64_t n_tokens, const void* table, int32_t 
 }
 
 size_t mdlm_embed_grad_workspace_bytes(int64_t n_tokens, int32_t H) {
-  if (n_tokens > INT32_MAX) return 0;
+  if (n_tokens > INT32_MAX || H > kEmbedMaxH) return 0;
   return embed_grad_workspace_bytes(n_tokens, H);
 }
 
@@ -479,6 +480,7 @@ int mdlm_embed_grad(const int32_t* ids, int64_t n_tokens, const void* d_out, int
   const char* fn = "mdlm_embed_grad";
   const hipStream_t st = reinterpret_cast<hipStream_t>(stream);
   if (const int rc = check_row_sizes(fn, dtype, n_tokens, H)) return rc;
+  if (H > kEmbedMaxH) return fail(MDLM_EUNSUPPORTED, "%s: H = %d exceeds %d", fn, H, kEmbedMaxH);
   if (V <= 0) return fail(MDLM_EINVAL, "%s: V must be > 0", fn);
   if (!isfinite(scale)) return fail(MDLM_EINVAL, "%s: scale must be finite", fn);
   if (accumulate != 0 && accumulate != 1)

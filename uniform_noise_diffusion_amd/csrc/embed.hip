@@ -230,10 +230,11 @@ merge_lds_kernel(const int32_t* __restrict__ sid, const int32_t* __restrict__ sp
 }
 
 // Merges up to kFan sorted runs of `len` entries into one, as above, in
-// memory.  A wave holds 64 neighbours of one run, so in another run all their places lie between those of its first and its last
-// key: one round of 64 probes of every run bounds both, and the lanes' own
-// searches are confined to what lies between.  (Each lane searching the whole
-// runs is bound by the gathers: 27 us at 65,536 tokens.)
+// memory.  A wave holds 64 neighbours of one run, so in another run all their
+// places lie between those of its first and its last key: one round of 64
+// probes of every run bounds both, and the lanes' own searches are confined to
+// what lies between.  (Each lane searching the whole runs is bound by the
+// gathers: 27 us at 65,536 tokens.)
 __device__ __forceinline__ bool comes_before(int32_t v, int64_t r, int32_t id, int64_t run) {
   return v < id || (v == id && r < run);
 }
@@ -448,7 +449,7 @@ join_runs_kernel(const int32_t* __restrict__ sid, int64_t n, int32_t V, int32_t 
                  int64_t part_pitch, const uint8_t* __restrict__ cut) {
   __shared__ int32_t s_short[kJoinThreads], s_long[kJoinThreads];
   __shared__ int32_t s_count[2][kJoinWaves];
-  __shared__ float s_sum[64][64];
+  __shared__ __align__(16) float s_sum[64][64];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int64_t chunks = (n + C - 1) / C;
@@ -693,21 +694,31 @@ few_tokens_kernel(const int32_t* __restrict__ ids, int32_t n, int32_t V, int32_t
 // 34 against 15).
 bool is_few(int64_t n, int32_t H) { return n <= kFewTokens && n * H <= (int64_t)1 << 20; }
 
+// Rows and number of the blocks that clear the table beside few tokens' sums:
+// 64 KiB to a block, as far as its 64 bits for the rows go.
+int few_rows(int32_t H) { return std::max(1, std::min(64, 16384 / H)); }
+int64_t few_fills(int32_t V, int32_t H) { return ((int64_t)V + few_rows(H) - 1) / few_rows(H); }
+
 template <typename T, bool FULL>
 void run_few(const int32_t* ids, int64_t n, int32_t V, int32_t H, const void* d_out, float scale,
              float* d_table, bool accumulate, bool fill, hipStream_t stream) {
   const T* g = reinterpret_cast<const T*>(d_out);
   const int slabs = (H + kFewCols - 1) / kFewCols;
   const int sums = (int)((n + kFewWaves - 1) / kFewWaves) * slabs;
-  const int rows = std::max(1, std::min(64, 16384 / H));  // 64 KiB to a clearing block
-  const int fills = fill ? (V + rows - 1) / rows : 0;
+  const int rows = few_rows(H);
+  const int fills = fill ? (int)few_fills(V, H) : 0;
   auto kernel = accumulate ? few_tokens_kernel<T, FULL, true> : few_tokens_kernel<T, FULL, false>;
   kernel<<<(unsigned)(sums + fills), kFewThreads, 0, stream>>>(ids, (int32_t)n, V, H, slabs, g,
                                                                scale, d_table, sums, rows);
 }
 
-// Floats of a table that the sorting launch clears.
+// Floats of a table that the sorting launch clears, and blocks that may clear
+// it beside few tokens' sums (two per compute unit).  A call into 16,384 x 64
+// (256 blocks) takes 5.2 us so and 8.3 with a launch to clear the table; into
+// 32,768 x 512 (1,024 blocks) 14.2 and 13.4, into 2,097,152 x 8 (32,768 blocks
+// of 64 short rows) 153 and 13.4.
 constexpr int64_t kSmallTable = (int64_t)16 << 20;
+constexpr int64_t kFewFills = 512;
 
 // Entries of the sorted list per chunk: the most, up to 32, that leave 2,048
 // waves (two per SIMD) something to do, and four at the least.
@@ -786,7 +797,8 @@ hipError_t launch_embed_grad(const int32_t* ids, int64_t n, const void* d_out, i
   uint8_t* cut = reinterpret_cast<uint8_t*>(ws + 4 * list);
   float* part = reinterpret_cast<float*>(ws + 4 * list + round_up((n + C - 1) / C, 256));
   const int64_t table_n = (int64_t)V * H;
-  const bool apart = n == 0 || table_n > kSmallTable;
+  const bool apart =
+      n == 0 || (is_few(n, H) ? few_fills(V, H) > kFewFills : table_n > kSmallTable);
   if (!accumulate && apart)
     clear_kernel<<<(unsigned)std::min<int64_t>(table_n / 4 / kThreads + 1, (int64_t)1 << 23),
                    kThreads, 0, stream>>>(d_table, table_n);

@@ -219,6 +219,9 @@ size_t embed_grad_workspace_bytes(int64_t n, int32_t H);
 hipError_t launch_embed_grad(const int32_t* ids, int64_t n, const void* d_out, int32_t dtype,
                              int32_t V, int32_t H, float scale, float* d_table, bool accumulate,
                              void* workspace, hipStream_t stream);
+// Rows of at most kEmbedMaxH entries (a launch counts 2,048 of them per block
+// in its second dimension).
+constexpr int32_t kEmbedMaxH = 1 << 26;
 // Rows of at most kNormMaxH entries (16 waves hold one row in registers).
 constexpr int32_t kNormMaxH = 16384;
 hipError_t launch_norm_fwd(const void* x, int32_t dtype, int64_t n, int32_t H, int32_t kind,
