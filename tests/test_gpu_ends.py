@@ -100,6 +100,8 @@ def test_step_refuses_what_it_was_not_made_for():
     x, w = torch.zeros_like(step.embedded), torch.ones(64, device=DEV, dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="norm_bias"):
         step.final_norm(x, w, w)
+    with pytest.raises(RuntimeError, match="head_ce_dw"):
+        step.embed_grad(x)
 
 
 def test_captured_step_replays_match_eager():

@@ -128,6 +128,7 @@ class MdlmTrainStep(MdlmLossStep):
         self.norm_ws = torch.empty(max(B.mdlm_norm_bwd_workspace_bytes(n_tokens, H), 1), **u8)
         self.embed_ws = torch.empty(max(B.mdlm_embed_grad_workspace_bytes(n_tokens, H), 1), **u8)
         self._norm_weight = None
+        self._dW_written = False
 
     def embed(self, table, stream=None):
         """The corrupted tokens' embeddings into `embedded`."""
@@ -149,6 +150,7 @@ class MdlmTrainStep(MdlmLossStep):
         B.mdlm_fused_head_ce_fwd_bwd_dw(self.hidden, W, self.row_idx, self.tgt, self.w,
                                         self.n_rows, self.n_tokens, softcap, self.loss,
                                         self.row_ce, self.d_hidden, self.dW, self.head_ws, stream)
+        self._dW_written = True
         return self.loss
 
     def norm_grad(self, stream=None):
@@ -166,6 +168,8 @@ class MdlmTrainStep(MdlmLossStep):
     def embed_grad(self, d_embedded, stream=None):
         """The table's gradient from the gradient of `embedded`: added to `dW`
         (tied) or written to `d_table`."""
+        if self.tied and not self._dW_written:
+            raise RuntimeError("embed_grad() of a tied table follows head_ce_dw()")
         B.mdlm_embed_grad(self.xt, d_embedded, self.embed_scale, self.d_table,
                           accumulate=self.tied, workspace=self.embed_ws, stream=stream)
         return self.d_table
