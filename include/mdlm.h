@@ -582,8 +582,11 @@ enum { MDLM_NORM_LAYER = 0, MDLM_NORM_RMS = 1 };
  *   RMS:   mean = 0,           rstd = 1 / sqrt(mean(x_row^2) + eps)
  *   y = (x - mean) * rstd * weight + bias
  *
- * in fp32 throughout, y rounded once to `dtype` (entries beyond 1e19, whose
- * squares overflow, make a variance of infinity).
+ * in fp32 throughout, y rounded once to `dtype`.  A row whose squares (LAYER:
+ * those of its distances from the mean, however large that is) sum to more
+ * than float's range, as beyond 1.8e19 each, has a variance of infinity: rstd
+ * is 0 and y the bias.  LAYER asks that the row's plain sum be in range too;
+ * y is NaN where it is not.
  *
  *   x           [n, H] row-major, element type `dtype`.
  *   dtype       MDLM_BF16 or MDLM_F32.

@@ -185,7 +185,8 @@ norm_fwd_kernel(const NormFwdArgs a) {
         mean = s * a.inv_h;
 #pragma unroll
         for (int w = 0; w < W; ++w) {
-          const float d = s_part[flip][2][w0 + w] - mean;
+          // (a wave past the row's end has no columns, and no mean either)
+          const float d = 512 * w < H ? s_part[flip][2][w0 + w] - mean : 0.f;
           m2 += s_cols[w0 + w] * (d * d);
         }
       }
