@@ -6,7 +6,8 @@ import numpy as np
 import pytest
 import torch
 
-from ends_common import DEV, Guarded, f64, norm_bounds, to_dev, within
+from ends_common import (DEV, Guarded, f64, norm_bounds, norm_grad_bounds, to_dev,
+                         within)
 from oracle import ends
 from uniform_noise_diffusion_amd import binding as B
 
@@ -68,3 +69,42 @@ def test_forward_of_a_sum_past_the_range(dtype, H):
     B.mdlm_norm_fwd(x, B.MDLM_NORM_LAYER, None, None, EPS, y)
     assert torch.isnan(y[1]).all()
     assert torch.equal(y[::2], alone[::2])
+
+
+# Widths with lanes past the row's end that hold whole eights of no column, or
+# an eight that the row only begins.
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("source", ["x", "checkpoint"])
+@pytest.mark.parametrize("H", [1, 4, 9, 1001, 1100, 2053, 8195])
+def test_backward_of_a_row_whose_mean_times_rstd_overflows(dtype, source, H):
+    """A constant row of 2^120 with rstd = 1 / sqrt(1e-5): (0 - mean) * rstd is
+    infinite, but no entry of the row is 0 and xhat is 0 in all of it.  A row of
+    ordinary values beside it."""
+    g = torch.Generator(device=DEV).manual_seed(H)
+    x = torch.randn(2, H, device=DEV, generator=g)
+    if source == "checkpoint":  # values an 8-bit checkpoint holds exactly
+        x = x.to(torch.float8_e4m3fn).float()
+    x[0] = 2.0 ** 120
+    x = x.to(dtype)
+    x64 = f64(x)
+    dy = torch.randn(2, H, device=DEV, generator=g).to(dtype)
+    w = torch.randn(H, device=DEV, generator=g).to(dtype)
+    _, mu, r = ends.norm(x64, B.MDLM_NORM_LAYER, None, None, EPS)
+    mean, mu64 = to_dev(mu, torch.float32)
+    rstd, r64 = to_dev(r, torch.float32)
+    assert mu64[0] == 2.0 ** 120 and mu64[0] * r64[0] > torch.finfo(torch.float32).max
+    dx = torch.empty_like(x)
+    dw, db = torch.empty(H, device=DEV), torch.empty(H, device=DEV)
+    if source == "checkpoint":
+        q = torch.empty(2, H, dtype=torch.uint8, device=DEV)
+        q_exp = torch.empty(2, -(-H // 128), dtype=torch.uint8, device=DEV)
+        B.mdlm_ckpt8_save(x, q, q_exp)
+        x64 = ends.ckpt8_load(q.cpu().numpy(), q_exp.cpu().numpy())
+        assert (x64[0] == 2.0 ** 120).all()
+        B.mdlm_norm_bwd_ckpt8(dy, q, q_exp, B.MDLM_NORM_LAYER, w, mean.t, rstd.t, dx, dw, db)
+    else:
+        B.mdlm_norm_bwd(dy, x, B.MDLM_NORM_LAYER, w, mean.t, rstd.t, dx, dw, db)
+    want = ends.norm_grad(f64(dy), x64, B.MDLM_NORM_LAYER, f64(w), mu64, r64)
+    bound = norm_grad_bounds(f64(dy), x64, B.MDLM_NORM_LAYER, f64(w), mu64, r64, dtype)
+    for t, a, d in zip((dx, dw, db), want, bound):
+        within(f64(t), a, d, H)

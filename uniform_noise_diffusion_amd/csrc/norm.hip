@@ -320,16 +320,17 @@ norm_bwd_kernel(const NormBwdArgs a) {
         float t1 = 0.f, t2 = 0.f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          xh[k][i] = (xh[k][i] - mean) * r;
+          // (an entry past the row's end is no part of it: its distance from
+          // the mean may be past float's range where every column's is not)
+          xh[k][i] = FULL || c0 + 512 * W * k + i < H ? (xh[k][i] - mean) * r : 0.f;
           dw[k][i] += g[k][i] * xh[k][i];
           db[k][i] += g[k][i];
           g[k][i] *= wt[k][i];
           t1 += g[k][i];
           t2 += g[k][i] * xh[k][i];
         }
-        // lanes past the row's end: see above, or (not FULL) dy = 0, which
-        // adds nothing unless the row's statistics, and with them its
-        // results, are not finite
+        // lanes past the row's end: see above, or (not FULL) dy = 0 and
+        // xhat = 0, which add nothing
         const bool counts = !FULL || c0 + 512 * W * k < H;
         s1 += counts ? t1 : 0.f;
         s2 += counts ? t2 : 0.f;
