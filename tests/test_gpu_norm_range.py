@@ -108,3 +108,13 @@ def test_backward_of_a_row_whose_mean_times_rstd_overflows(dtype, source, H):
     bound = norm_grad_bounds(f64(dy), x64, B.MDLM_NORM_LAYER, f64(w), mu64, r64, dtype)
     for t, a, d in zip((dx, dw, db), want, bound):
         within(f64(t), a, d, H)
+
+
+def test_sums_over_no_rows_leave_the_gradients_bits():
+    """n = 0, accumulating: not even a zero's sign changes."""
+    x, stat = torch.empty(0, 3, device=DEV), torch.empty(0, device=DEV)
+    start = torch.tensor([-0.0, 1.5, float("nan")], device=DEV)
+    dw, db = start.clone(), start.clone()
+    B.mdlm_norm_bwd(x, x, B.MDLM_NORM_RMS, None, None, stat, None, dw, db, accumulate=True)
+    for t in (dw, db):
+        assert torch.equal(t.view(torch.int32), start.view(torch.int32))

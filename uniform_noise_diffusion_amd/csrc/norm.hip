@@ -548,7 +548,8 @@ hipError_t launch_norm_bwd(const void* dy, const void* x, const uint8_t* q, cons
                    : (dtype == MDLM_BF16 ? pick_bwd<bf16_t, false> : pick_bwd<float, false>);
     run(a, (unsigned)blocks, stream);
   }
-  if ((d_weight || d_bias) && !direct)
+  // (no rows, accumulating: nothing to add, and + 0 would clear a zero's sign)
+  if ((d_weight || d_bias) && !direct && (n > 0 || !accumulate))
     norm_sum_kernel<<<dim3((H + 63) / 64, 2), kSumWaves * 64, 0, stream>>>(
         a.part_w, a.part_b, (int32_t)blocks, H, d_weight, d_bias, accumulate);
   return hipGetLastError();
