@@ -127,7 +127,8 @@ class MdlmTrainStep(MdlmLossStep):
         self.d_table = self.dW if tied else torch.empty((V, H), **f32)
         self.norm_ws = torch.empty(max(B.mdlm_norm_bwd_workspace_bytes(n_tokens, H), 1), **u8)
         self.embed_ws = torch.empty(max(B.mdlm_embed_grad_workspace_bytes(n_tokens, H), 1), **u8)
-        self._norm_weight = None
+        self._normed = False
+        self._norm_weight = None  # (of the last final_norm(): None is a weight of 1)
         self._dW_written = False
 
     def embed(self, table, stream=None):
@@ -140,7 +141,7 @@ class MdlmTrainStep(MdlmLossStep):
         as an 8-bit checkpoint."""
         if (bias is None) != (self.d_norm_bias is None):
             raise ValueError("bias: given exactly when the step was made with norm_bias=True")
-        self._norm_weight = weight
+        self._normed, self._norm_weight = True, weight
         B.mdlm_norm_fwd(x, self.norm_kind, weight, bias, self.norm_eps, self.hidden, self.mean,
                         self.rstd, self.q, self.q_exp, stream)
         return self.hidden
@@ -157,7 +158,7 @@ class MdlmTrainStep(MdlmLossStep):
         """`d_last` (the gradient that enters the model's layers) and the norm's
         own gradients from `d_hidden` and the checkpoint of the last
         final_norm()."""
-        if self._norm_weight is None:
+        if not self._normed:
             raise RuntimeError("norm_grad() follows final_norm()")
         B.mdlm_norm_bwd_ckpt8(self.d_hidden, self.q, self.q_exp, self.norm_kind,
                               self._norm_weight, self.mean, self.rstd, self.d_last,
