@@ -10,6 +10,7 @@ implementation.
 
 import ctypes
 import functools
+import operator
 import os
 
 import torch
@@ -82,6 +83,19 @@ EXPORTED = (
 
 _lib = None
 
+_I32_MAX = 0x7FFFFFFF
+
+
+class _Int32:
+    """Type of the library's int32_t arguments: ctypes' own keeps the low 32
+    bits of a larger number and says nothing."""
+
+    @staticmethod
+    def from_param(value):
+        if -_I32_MAX - 1 <= value <= _I32_MAX:
+            return operator.index(value)
+        raise ValueError(f"{value} does not fit 32 bits")
+
 
 class MdlmError(RuntimeError):
     def __init__(self, code, message):
@@ -99,7 +113,7 @@ def load():
             f"{LIB_PATH} is missing: build it with "
             "`python -m uniform_noise_diffusion_amd.build`")
     lib = ctypes.CDLL(LIB_PATH)
-    vp, i32, i64, u64, f32, f64, sz = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64,
+    vp, i32, i64, u64, f32, f64, sz = (ctypes.c_void_p, _Int32, ctypes.c_int64,
                                        ctypes.c_uint64, ctypes.c_float, ctypes.c_double,
                                        ctypes.c_size_t)
     lib.mdlm_corrupt.argtypes = [vp, i64, vp, i32, u64, f64, i32, i32, i32, vp, vp, vp, vp, vp]
@@ -492,7 +506,22 @@ def _rows(x, name):
     if x.dim() == 0:
         raise ValueError(f"{name}: expected [..., H]")
     H = x.shape[-1]
+    _fits(H, name)
     return (x.numel() // H if H else 0), H
+
+
+def _fits(size, name):
+    if size > _I32_MAX:
+        raise ValueError(f"{name}: {size} does not fit 32 bits")
+
+
+def _table(t, name):
+    """(V, H) of a table."""
+    if t.dim() != 2:
+        raise ValueError(f"{name}: expected [V, H]")
+    V, H = t.shape
+    _fits(max(V, H), name)
+    return V, H
 
 
 def _launch(fn, dev, stream, *args):
@@ -531,9 +560,7 @@ def mdlm_embed(ids, table, scale, out, stream=None):
     """See mdlm_embed in include/mdlm.h: out[...] = scale * table[ids[...]].
     `ids` int32 of any shape; `table` [V, H] and `out` [*ids.shape, H] bf16 or
     float32."""
-    if table.dim() != 2:
-        raise ValueError("table: expected [V, H]")
-    V, H = table.shape
+    V, H = _table(table, "table")
     dt = dtype_code(table)
     dev = _place(table, "table")
     _launch(load().mdlm_embed, dev, stream, _arg(ids, "ids", torch.int32, ids.shape, dev),
@@ -550,9 +577,7 @@ def mdlm_embed_grad(ids, d_out, scale, d_table, accumulate=False, workspace=None
     """See mdlm_embed_grad in include/mdlm.h: `d_out` [*ids.shape, H] bf16 or
     float32, `d_table` [V, H] float32, overwritten or (accumulate) added to;
     `workspace` a uint8 tensor, allocated for the call if None."""
-    if d_table.dim() != 2:
-        raise ValueError("d_table: expected [V, H]")
-    V, H = d_table.shape
+    V, H = _table(d_table, "d_table")
     n = ids.numel()
     dt = dtype_code(d_out)
     dev = _place(d_out, "d_out")
@@ -592,9 +617,9 @@ def mdlm_norm_bwd_workspace_bytes(n, H):
     return load().mdlm_norm_bwd_workspace_bytes(int(n), int(H))
 
 
-def _norm_bwd(fn, dy, source, kind, weight, mean, rstd, dx, d_weight, d_bias, accumulate,
+def _norm_bwd(fn, rows, dy, source, kind, weight, mean, rstd, dx, d_weight, d_bias, accumulate,
               workspace, stream, dev):
-    n, H = _rows(dy, "dy")
+    n, H = rows
     T, lead, f32 = dy.dtype, dy.shape[:-1], torch.float32
     args = (_arg(dy, "dy", T, dy.shape, dev), *source, dtype_code(dy), n, H, int(kind),
             _arg(weight, "weight", T, (H,), dev), _arg(mean, "mean", f32, lead, dev),
@@ -614,18 +639,18 @@ def mdlm_norm_bwd(dy, x, kind, weight, mean, rstd, dx, d_weight=None, d_bias=Non
     `mean` (None for RMS) and `rstd` as mdlm_norm_fwd left them, `d_weight` and
     `d_bias` float32 [H]; outputs not wanted are None; `workspace` a uint8
     tensor, allocated for the call if None."""
-    dev = _place(dy, "dy")
-    _norm_bwd(load().mdlm_norm_bwd, dy, (_arg(x, "x", dy.dtype, dy.shape, dev),), kind, weight,
-              mean, rstd, dx, d_weight, d_bias, accumulate, workspace, stream, dev)
+    rows, dev = _rows(dy, "dy"), _place(dy, "dy")
+    _norm_bwd(load().mdlm_norm_bwd, rows, dy, (_arg(x, "x", dy.dtype, dy.shape, dev),), kind,
+              weight, mean, rstd, dx, d_weight, d_bias, accumulate, workspace, stream, dev)
 
 
 def mdlm_norm_bwd_ckpt8(dy, q, q_exp, kind, weight, mean, rstd, dx, d_weight=None, d_bias=None,
                         accumulate=False, workspace=None, stream=None):
     """See mdlm_norm_bwd_ckpt8 in include/mdlm.h: mdlm_norm_bwd with x as the
     8-bit checkpoint `q`, `q_exp` holds it."""
-    dev = _place(dy, "dy")
-    _norm_bwd(load().mdlm_norm_bwd_ckpt8, dy, _ckpt8_args(q, q_exp, dy.shape, dev), kind, weight,
-              mean, rstd, dx, d_weight, d_bias, accumulate, workspace, stream, dev)
+    rows, dev = _rows(dy, "dy"), _place(dy, "dy")
+    _norm_bwd(load().mdlm_norm_bwd_ckpt8, rows, dy, _ckpt8_args(q, q_exp, dy.shape, dev), kind,
+              weight, mean, rstd, dx, d_weight, d_bias, accumulate, workspace, stream, dev)
 
 
 def mdlm_ckpt8_save(x, q, q_exp, stream=None):
