@@ -664,7 +664,8 @@ int mdlm_norm_bwd_ckpt8(const void* dy, const uint8_t* q, const uint8_t* q_exp, 
  *               the two calls need not use the same).
  *   q           [n, H] bytes.
  *   q_exp       [n, ceil(H / 128)] bytes.
- *   n, H        n >= 0 and below 2^31, H > 0; n * ceil(H / 128) below 2^32.
+ *   n, H        n >= 0 and below 2^31, H > 0 and at most 2^31 - 128;
+ *               n * ceil(H / 128) below 2^32.
  * Returns MDLM_OK, MDLM_EINVAL, MDLM_EUNSUPPORTED or MDLM_EHIP.
  */
 int mdlm_ckpt8_save(const void* x, int32_t dtype, int64_t n, int32_t H, uint8_t* q,

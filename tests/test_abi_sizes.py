@@ -66,3 +66,19 @@ def test_numbers_past_int32(name):
         for value in (PAST, 1 << 31, -(1 << 31) - 1):
             with pytest.raises(ctypes.ArgumentError, match="32 bits"):
                 fn(*args[:i], value, *args[i + 1:])
+
+
+@pytest.mark.parametrize("H,code", [((1 << 31) - 1, B.MDLM_EUNSUPPORTED),
+                                    ((1 << 31) - 127, B.MDLM_EUNSUPPORTED),
+                                    ((1 << 31) - 128, B.MDLM_OK)])
+def test_checkpoint_rows_whose_last_block_ends_past_int32(H, code):
+    """Columns are counted in 32 bits up to the end of a row's last block of
+    128.  (Without rows nothing is launched.)"""
+    if not os.path.exists(B.LIB_PATH):
+        pytest.skip("libmdlm.so not built")
+    lib = B.load()
+    for dtype in (B.MDLM_BF16, B.MDLM_F32):
+        assert lib.mdlm_ckpt8_save(None, dtype, 0, H, None, None, None) == code
+        assert lib.mdlm_ckpt8_load(None, None, dtype, 0, H, None, None) == code
+    if code != B.MDLM_OK:
+        assert "exceeds 2147483520" in B.mdlm_last_error()

@@ -596,6 +596,7 @@ int mdlm_norm_bwd_ckpt8(const void* dy, const uint8_t* q, const uint8_t* q_exp, 
 static int check_ckpt8(const char* fn, const void* x, int32_t dtype, int64_t n, int32_t H,
                        const uint8_t* q, const uint8_t* q_exp) {
   if (const int rc = check_row_sizes(fn, dtype, n, H)) return rc;
+  if (H > kCkptMaxH) return fail(MDLM_EUNSUPPORTED, "%s: H = %d exceeds %d", fn, H, kCkptMaxH);
   if (n * (((int64_t)H + 127) / 128) > UINT32_MAX)
     return fail(MDLM_EUNSUPPORTED, "%s: 2^32 or more blocks of 128", fn);
   if (n > 0 && (!x || !q || !q_exp)) return fail(MDLM_EINVAL, "%s: null pointer", fn);

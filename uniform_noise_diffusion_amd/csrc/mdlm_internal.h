@@ -224,6 +224,9 @@ hipError_t launch_embed_grad(const int32_t* ids, int64_t n, const void* d_out, i
 constexpr int32_t kEmbedMaxH = 1 << 26;
 // Rows of at most kNormMaxH entries (16 waves hold one row in registers).
 constexpr int32_t kNormMaxH = 16384;
+// Rows of at most kCkptMaxH entries (columns are counted in 32 bits up to the
+// end of the last block of 128).
+constexpr int32_t kCkptMaxH = INT32_MAX - 127;
 hipError_t launch_norm_fwd(const void* x, int32_t dtype, int64_t n, int32_t H, int32_t kind,
                            const void* weight, const void* bias, double eps, void* y, float* mean,
                            float* rstd, uint8_t* q, uint8_t* q_exp, hipStream_t stream);
