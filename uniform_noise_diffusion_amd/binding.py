@@ -701,11 +701,13 @@ def mdlm_check_rows(row_idx, tgt, w, n_rows, max_rows, n_tokens, V, status, stre
 
 
 def mdlm_check_tokens(ids, V, status, stream=None):
-    """See mdlm_check_tokens in include/mdlm.h."""
-    _need(ids, torch.int32, "ids")
-    _need(status, torch.int32, "status")
-    _check(load().mdlm_check_tokens(_ptr(ids), ids.numel(), int(V), _ptr(status),
-                                    _stream(stream)))
+    """See mdlm_check_tokens in include/mdlm.h: `ids` int32 of any shape, `status`
+    a one-element int32 tensor on the same device."""
+    dev = _place(ids, "ids")
+    if status.numel() < 1:
+        raise ValueError("status: expected one element")
+    _launch(load().mdlm_check_tokens, dev, stream, _arg(ids, "ids", torch.int32, ids.shape, dev),
+            ids.numel(), int(V), _arg(status, "status", torch.int32, status.shape, dev))
 
 
 def mdlm_set_checking(enable):
