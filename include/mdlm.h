@@ -543,9 +543,11 @@ int mdlm_embed(const int32_t* ids, int64_t n_tokens, const void* table, int32_t 
  *
  *   d_table[v] = [accumulate] d_table[v] + scale * sum over ids[i] = v of d_out[i]
  *
- * The tokens are sorted by id (ties by position), so each row's terms are
- * summed in fp32 in an order that depends on the sizes alone: no atomics, the
- * same bits on every run.  Ids outside [0, V) count for nothing.
+ * The tokens are sorted by id (ties by position) and each row's terms summed
+ * in fp32 without atomics, in an order that the sizes and the ids determine:
+ * the same inputs give the same bits on every run.  (All ids: other rows' decide
+ * where this row's terms are cut into partial sums, so changing them may change
+ * its rounding.)  Ids outside [0, V) count for nothing.
  *
  *   ids, n_tokens, V, H, scale: as for mdlm_embed.
  *   d_out       [n_tokens, H], element type `dtype` (MDLM_BF16 or MDLM_F32).

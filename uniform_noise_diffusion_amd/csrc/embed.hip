@@ -11,12 +11,15 @@
 // Forward: a gather, bound by memory; a wave moves 2,048 entries of a row.
 //
 // Gradient: the tokens are sorted by id (position breaking ties), so each
-// table row's terms lie side by side and are summed in ascending position by
-// one wave per 512 columns: no atomics, and the same bits on every run.
-// Absorbing corruption makes about half of all tokens one id (the mask), so
-// the sorted list holds one run of n/2 among runs of one or two: the list is
-// cut into chunks of C entries, runs longer than a chunk are summed chunk by
-// chunk into partial rows, and a last kernel adds those in order.
+// table row's terms lie side by side: no atomics, and the same bits whenever
+// the sizes and the ids are the same.  Absorbing corruption makes about half of
+// all tokens one id (the mask), so the sorted list holds one run of n/2 among
+// runs of one or two: the list is cut into chunks of C entries.  A run within
+// two neighbouring chunks is summed in ascending position by one wave per 512
+// columns; a longer one is summed chunk by chunk into partial rows, which a last
+// kernel adds up (where it is cut, and so its rounding, depends on how many
+// tokens have lower ids).  Few tokens take one launch without a list, in which
+// four groups of lanes, or 16 waves, share a run.
 #include "row_ops.h"
 
 #include <algorithm>
@@ -103,7 +106,7 @@ __device__ __forceinline__ int count_below(const uint32_t* s_id, int q, uint32_t
 // LDS and ranks 16 tokens at a time, a lane comparing one of them with every
 // 64th group of four ids: two instructions per 64 comparisons, no exchange and
 // no barriers inside.  6.3 us at 4,096 tokens, of which the comparisons are
-// 1.8; 12 us at 8,192.  (A bitonic network of 1,024 took 14 us and left more
+// 1.8; 12 to 13 us at 8,192, where they are four times as many.  (A bitonic network of 1,024 took 14 us and left more
 // to merge; counting with ballots, whose bits the scalar unit adds up, 7.5
 // and 19 us.)
 __global__ void __launch_bounds__(kRankThreads)
@@ -688,10 +691,14 @@ few_tokens_kernel(const int32_t* __restrict__ ids, int32_t n, int32_t V, int32_t
   }
 }
 
-// Few enough for one launch: beyond about 2^20 entries the sorted list is
-// faster (H = 4,096, half of the tokens the mask, added to the table: 256
-// tokens 7.7 us a call against 14.3, 512 tokens 14.3 against 14.5, 1,024 tokens
-// 34 against 15).
+// Few enough for one launch: up to 2^20 entries it is the faster way at every
+// width, at twice that both are even, beyond the sorted list is.  us a call,
+// added to a table of 16,384 rows, with uniform ids / half of them one; the list
+// takes 14 to 15 in all of these:
+//   tokens       H = 8       64        256       1,024       4,096
+//      256    6.2/ 7.3   6.2/ 7.3   6.1/ 7.4   6.2/ 7.6    6.5/ 7.8
+//      512    6.3/ 7.9   6.2/ 7.9   6.3/ 8.1   6.3/ 8.3   12.8/13.7
+//    1,024    6.7/10.4   6.5/10.3   6.6/10.4   9.7/11.1   29.6/30.4
 bool is_few(int64_t n, int32_t H) { return n <= kFewTokens && n * H <= (int64_t)1 << 20; }
 
 // Rows and number of the blocks that clear the table beside few tokens' sums:
@@ -713,10 +720,10 @@ void run_few(const int32_t* ids, int64_t n, int32_t V, int32_t H, const void* d_
 }
 
 // Floats of a table that the sorting launch clears, and blocks that may clear
-// it beside few tokens' sums (two per compute unit).  A call into 16,384 x 64
-// (256 blocks) takes 5.2 us so and 8.3 with a launch to clear the table; into
-// 32,768 x 512 (1,024 blocks) 14.2 and 13.4, into 2,097,152 x 8 (32,768 blocks
-// of 64 short rows) 153 and 13.4.
+// it beside few tokens' sums (two per compute unit).  A call with one token into
+// 16,384 x 64 (256 blocks) takes 5.9 us so and 8.8 with a launch to clear the
+// table; into 32,768 x 512 (1,024 blocks) 14.2 and 13.4, into 2,097,152 x 8
+// (32,768 blocks of 64 short rows) 153 and 13.4.
 constexpr int64_t kSmallTable = (int64_t)16 << 20;
 constexpr int64_t kFewFills = 512;
 
