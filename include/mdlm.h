@@ -587,8 +587,8 @@ enum { MDLM_NORM_LAYER = 0, MDLM_NORM_RMS = 1 };
  * in fp32 throughout, y rounded once to `dtype`.  A row whose squares (LAYER:
  * those of its distances from the mean, however large that is) sum to more
  * than float's range, as beyond 1.8e19 each, has a variance of infinity: rstd
- * is 0 and y the bias.  LAYER asks that the row's plain sum be in range too;
- * y is NaN where it is not.
+ * is 0 and y the bias.  LAYER asks that the row's magnitudes sum to a float
+ * too; y may be NaN where they do not.
  *
  *   x           [n, H] row-major, element type `dtype`.
  *   dtype       MDLM_BF16 or MDLM_F32.
