@@ -836,8 +836,9 @@ int mdlm_mx_product(const uint8_t* a, const uint8_t* a_exp, int32_t a_format, in
  * own log-probability of it (temperature 1, nothing left out).
  *
  * Weights are formed and summed in fp64 (or as 64-bit integers), in an order that
- * the sizes determine: the same inputs give the same token.  A NaN logit counts
- * as -inf, and -inf is never drawn.  A row without a logit above -inf gives token
+ * the sizes determine: the same inputs give the same token.  A weight under
+ * 2^-990 counts as zero, and is never drawn.  A NaN logit counts as -inf, and
+ * -inf is never drawn.  A row without a logit above -inf gives token
  * -1 and logp -inf.  Where logits are +inf, they share the row evenly.
  *
  *   logits      row j at logits + j * stride entries, element type `dtype`

@@ -17,7 +17,10 @@
 // far beyond what a comparison with u could tell apart by chance: weights are
 // formed in fp64.  Sums over a row are fp64 sums in an order that the sizes
 // determine; what is summed with atomics is summed as 64-bit integers, in units
-// of about 2^-61 of the whole, whose order does not matter.
+// of about 2^-61 of the whole, whose order does not matter.  The token is looked
+// for by fp64 sums alone, from the parts of the row down: a part may be lighter
+// than any unit of the whole, and u = 0 asks for the first token that weighs
+// anything.
 //
 // A row is never sorted.  What is read from memory counts (a pass costs what the
 // caches cannot hold), so a row takes two passes:
@@ -203,6 +206,8 @@ struct Ask {
     u = fminf(fmaxf(a.u[j], 0.f), 0x1.fffffep-1f);
     per_f = greedy ? 0.f : fminf(kLog2e / temp, 1e30f);
   }
+  // u's place is under what units of the whole can tell apart
+  __device__ __forceinline__ bool faint() const { return u < 0x1p-30f; }
   // u's place in a sum of units
   __device__ __forceinline__ u64 place(u64 sum) const { return (u64)((double)u * (double)sum); }
   // where top-p's tokens end: the first ones that reach this sum
@@ -221,7 +226,7 @@ struct Row {
   float below;    // logits under this one are certainly not kept
   uint32_t key;   // the cut: kept are larger keys, and this one up to `index`
   int index;
-  bool ties_only; // units are 1 where the key is `key`, else 0
+  bool ties_only; // weights are 1 where the key is `key`, else 0
   const double* table;
   __device__ __forceinline__ Row(const Ask& ask, float top_, int V, const double* table_)
       : top(top_), shift(0), min_w(ask.min_w), below(-kInf), key(0), index(V), ties_only(false),
@@ -246,7 +251,9 @@ struct Row {
 // (4e-17 remain after the 4th term).  n is formed by adding 1.5 * 2^52 and taken
 // from the sum's low bits, and the power of two is added to the entry's
 // exponent: rounding, conversion and ldexp would each take four times as long.
-// It never becomes zero, 2^-996 being the least; sums under 1e-200 count as none.
+// It never becomes zero, 2^-996 being the least; where a token is looked for, what
+// is under kLeast counts as zero.
+constexpr double kLeast = 0x1p-990;
 __device__ __forceinline__ double scaled_weight(const Row& r, float x, int shift) {
   constexpr double kMagic = 0x1.8p52, c = 0.693147180559945309417 / 256.0;
   const double d = fmin((double)r.top - (double)x, r.far);
@@ -272,18 +279,27 @@ __device__ __forceinline__ u64 to_units(double s) {  // s below 2^62
 __device__ __forceinline__ u64 units_of(const Row& r, float x) {
   return to_units(scaled_weight(r, x, r.shift));
 }
-__device__ __forceinline__ u64 kept_units(const Row& r, float x, int i) {
+__device__ __forceinline__ bool within_cut(const Row& r, float x, int i) {
   const uint32_t k = key_of(x);
-  if (r.ties_only) return k == r.key;
-  if (!(k > r.key || (k == r.key && i <= r.index))) return 0;
+  return k > r.key || (k == r.key && i <= r.index);
+}
+__device__ __forceinline__ u64 kept_units(const Row& r, float x, int i) {
+  if (!within_cut(r, x, i)) return 0;
   return r.min_w > 0.0 && weight_of(r, x) < r.min_w ? 0 : units_of(r, x);
 }
+__device__ __forceinline__ double kept_weight(const Row& r, float x, int i) {
+  if (r.ties_only) return key_of(x) == r.key ? 1.0 : 0.0;
+  if (!within_cut(r, x, i)) return 0.0;
+  const double w = weight_of(r, x);
+  return w < kLeast || w < r.min_w ? 0.0 : w;
+}
 
-__device__ __forceinline__ u64 scan64(u64 x) {  // inclusive, over the wave
+template <typename X>
+__device__ __forceinline__ X scan64(X x) {  // inclusive, over the wave
   const int lane = threadIdx.x & 63;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
-    const u64 y = __shfl_up(x, d, 64);
+    const X y = __shfl_up(x, d, 64);
     if (lane >= d) x += y;
   }
   return x;
@@ -923,94 +939,100 @@ __device__ __forceinline__ int draw_from_list(const Ask& ask, Row r, int n, doub
   return (int)(uint32_t)e;
 }
 
-// The waves' kept units over [lo, hi), into s.part; their total.
-template <typename T>
-__device__ __forceinline__ u64 part_sums(const T* row, const Row& r, int lo, int hi, Shared& s) {
+// One lane's sum of f(x, i) over the logits of a wave's share of [lo, hi) that r
+// may keep.
+template <typename X, typename T, typename F>
+__device__ __forceinline__ X share_sum(const T* row, const Row& r, int lo, int hi, F f) {
   constexpr int N = Vec<T>::n;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   int from, to;
   share<T>(wave, lo, hi, &from, &to);
-  u64 sum = 0;
+  X sum = 0;
   each_vec<T, kFew64<T>>(row, from, to, [&](const float* v, int i)
                          __attribute__((always_inline)) {
     if (most_of<N>(v) < r.below) return;
 #pragma unroll
     for (int k = 0; k < N; ++k)
-      if (v[k] >= r.below) sum += kept_units(r, v[k], i + k);
+      if (v[k] >= r.below) sum += f(v[k], i + k);
   });
-  sum = sum_of(sum);
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) s.part[threadIdx.x >> 6] = sum;
-  __syncthreads();
-  u64 all = 0;
-#pragma unroll
-  for (int w = 0; w < kWaves; ++w) all += s.part[w];
-  return all;
+  return sum;
+}
+// The waves' kept weights over [lo, hi), into s.weigh; their total.
+template <typename T>
+__device__ __forceinline__ double part_sums(const T* row, const Row& r, int lo, int hi, Shared& s) {
+  return weigh_waves(share_sum<double>(row, r, lo, hi,
+                                       [&](float x, int i) __attribute__((always_inline)) {
+                                         return kept_weight(r, x, i);
+                                       }),
+                     s);
 }
 
-// The first token of [lo, hi) up to which the kept units sum to more than t
-// (the last kept one at most).
+// Where t falls among `n` parts of these weights: the first one up to which they
+// sum to more than t, or the last that weighs anything (a sum taken in another
+// order may leave t no less than the whole), and in *t what of it lies in that
+// part.  -1: none weighs anything.
+__device__ __forceinline__ int part_at(const double* weight, int n, double* t) {
+  double before = 0.0, upto = 0.0;
+  int part = -1;
+  for (int k = 0; k < n && !(upto > *t); ++k) {
+    if (!(weight[k] > 0.0)) continue;
+    part = k, before = upto, upto += weight[k];
+  }
+  *t = fmax(*t - before, 0.0);
+  return part;
+}
+
+// The first token of [lo, hi) up to which the kept weights sum to more than t
+// (the last kept one at most); -1: none is kept.
 template <typename T>
-__device__ __forceinline__ int descend(const T* row, const Row& r, int lo, int hi, u64 t, Shared& s) {
+__device__ __forceinline__ int descend(const T* row, const Row& r, int lo, int hi, double t, Shared& s) {
   constexpr int N = Vec<T>::n;
   const int lane = threadIdx.x & 63;
   while (hi - lo > 64 * N) {
-    const u64 all = part_sums<T>(row, r, lo, hi, s);
-    if (all > 0) t = min(t, all - 1);
-    u64 before = 0;
-    int w = 0;
-    for (; w < kWaves - 1; ++w) {
-      const u64 p = s.part[w];
-      if (before + p > t) break;
-      before += p;
+    part_sums<T>(row, r, lo, hi, s);
+    const int w = part_at(s.weigh, kWaves, &t);
+    if (w < 0) {
+      __syncthreads();
+      return -1;
     }
     int from, to;
     share<T>(w, lo, hi, &from, &to);
-    t -= before;
     lo = from, hi = to;
   }
   // (every wave does the same)
-  u64 mine[N], sum = 0;
+  double mine[N], sum = 0.0;
   const int i = lo + lane * N;
 #pragma unroll
   for (int k = 0; k < N; ++k) {
     const float x = i + k < hi ? fmaxf((float)row[i + k], -kInf) : -kInf;
-    mine[k] = i + k < hi && x >= r.below ? kept_units(r, x, i + k) : 0;
+    mine[k] = i + k < hi && x >= r.below ? kept_weight(r, x, i + k) : 0.0;
     sum += mine[k];
   }
-  const u64 upto = scan64(sum);
-  const u64 all = __shfl(upto, 63, 64);
-  if (all > 0) t = min(t, all - 1);
-  const u64 hit = __ballot(upto > t);
-  const int from = hit ? __ffsll(hit) - 1 : 63;
-  u64 before = upto - sum;
-  int at = i;
+  const double upto = scan64(sum);
+  double before = __shfl_up(upto, 1, 64);
+  if (lane == 0) before = 0.0;
+  // (sums round: a token is taken only if it weighs something itself)
+  const u64 any = __ballot(sum > 0.0), hit = __ballot(sum > 0.0 && upto > t);
+  int at = -1;
+  bool past = false;
 #pragma unroll
   for (int k = 0; k < N; ++k) {
     before += mine[k];
-    at += before <= t ? 1 : 0;
+    if (mine[k] > 0.0 && !past) at = i + k, past = before > t;
   }
   __syncthreads();
-  return min(__shfl(at, from, 64), hi - 1);
+  return any ? __shfl(at, hit ? __ffsll(hit) - 1 : 63 - __clzll((long long)any), 64) : -1;
 }
 
-// Where u falls among `n` parts of these weights: the part, and what of it lies
-// before, in units.
-__device__ __forceinline__ int part_of(const Ask& ask, const Row& r, const double* weight, int n,
-                                       u64* inside) {
+// Where u falls among the row's `n` parts of these weights: the part, and in *t
+// what of it lies there.  -1, and *t in the whole row, where u's place is so near
+// the row's start that what the parts leave out (a list's units, what is
+// kLeast or less) could decide.
+__device__ __forceinline__ int part_of(const Ask& ask, const double* weight, int n, double* t) {
   double all = 0.0;
   for (int k = 0; k < n; ++k) all += weight[k];
-  const double t = (double)ask.u * all;
-  double before = 0.0;
-  int part = 0;
-  for (int k = 0; k < n; ++k) {
-    if (!(weight[k] > 1e-200)) continue;
-    part = k;
-    if (before + weight[k] > t) break;
-    before += weight[k];
-  }
-  *inside = to_units(fmin(ldexp(fmax(t - before, 0.0), r.shift), 0x1p61));
-  return part;
+  *t = (double)ask.u * all;
+  return ask.faint() ? -1 : part_at(weight, n, t);
 }
 
 // Writes a row's answer.  n_top: how many logits are infinite, if any is.
@@ -1105,17 +1127,18 @@ sample_row_kernel(const SampleArgs a, RowState* __restrict__ states) {
           }
         }
       }
-      if (!parts && token < 0) route = kGeneral;
     } else {
       r.scale(weigh_waves(weigh<T>(row, r, 0, V), s));
       parts = true;
     }
     if (parts) {
-      u64 t;
-      int lo, hi;
-      share<T>(part_of(ask, r, s.weigh, kWaves, &t), 0, V, &lo, &hi);
+      double t;
+      int lo = 0, hi = V;
+      const int part = part_of(ask, s.weigh, kWaves, &t);
+      if (part >= 0) share<T>(part, 0, V, &lo, &hi);
       token = descend<T>(row, r, lo, hi, t, s);
     }
+    if (token < 0) route = kGeneral;
   }
   if (threadIdx.x == 0) {
     states[j].found = f;
@@ -1285,9 +1308,10 @@ sample_third_kernel(const SampleArgs a, RowState* __restrict__ states, const Seg
     if (threadIdx.x < kMaxSegments)
       weight[threadIdx.x] += ldexp((double)units[threadIdx.x], -r.shift);
     __syncthreads();
-    u64 t;
-    const int k = part_of(ask, r, weight, g.per_row, &t);
-    const int lo = min(V, k * g.size), hi = min(V, lo + g.size);
+    double t;
+    int lo = 0, hi = V;
+    const int k = part_of(ask, weight, g.per_row, &t);
+    if (k >= 0) lo = min(V, k * g.size), hi = min(V, lo + g.size);
     token = descend<T>(row, r, lo, hi, t, s);
   }
   if (threadIdx.x == 0) states[j].route = token < 0 ? kGeneral : kDone;
@@ -1420,7 +1444,7 @@ __device__ __forceinline__ void cut(const T* row, Row& r, const Ask& ask, bool b
     ties.below = value_of(in.prefix);
     const u64 each = by_count ? 1 : units_of(r, value_of(in.prefix));
     const u64 n = each ? (need + each - 1) / each : inside;
-    r.index = descend<T>(row, ties, 0, V, max((u64)1, min(n, inside)) - 1, s);
+    r.index = descend<T>(row, ties, 0, V, (double)(max((u64)1, min(n, inside)) - 1), s);
     r.key = in.prefix;
     r.below = fmaxf(r.below, ties.below);
     return;
@@ -1457,11 +1481,11 @@ __device__ __forceinline__ void rest_of_row(const SampleArgs& a, int64_t j, cons
     r.ties_only = true;
     r.key = key_of(f.top);
     r.below = f.top;
-    n_top = part_sums<T>(row, r, 0, V, s);
+    n_top = (u64)part_sums<T>(row, r, 0, V, s);
     u64 n = ask.greedy ? 1 : n_top;
     if (ask.by_k) n = min(n, (u64)ask.k);
     if (ask.by_p) n = ask.goal(n);
-    token = descend<T>(row, r, 0, V, ask.place(n), s);
+    token = descend<T>(row, r, 0, V, (double)ask.u * (double)n, s);
   } else {
     const double min_w = r.min_w;
     const float below = r.below;
@@ -1470,12 +1494,16 @@ __device__ __forceinline__ void rest_of_row(const SampleArgs& a, int64_t j, cons
     u64 all = 0;
     if (ask.by_k) {
       cut<T>(row, r, ask, true, (u64)ask.k, V, s);
-      if (ask.by_p) all = part_sums<T>(row, r, 0, V, s);
+      if (ask.by_p)
+        all = block_sum(share_sum<u64>(row, r, 0, V,
+                                       [&](float x, int i) __attribute__((always_inline)) {
+                                         return kept_units(r, x, i);
+                                       }),
+                        s);
     }
     if (ask.by_p) cut<T>(row, r, ask, false, ask.by_k ? ask.goal(all) : 0, V, s);
     r.min_w = min_w, r.below = fmaxf(r.below, below);
-    all = part_sums<T>(row, r, 0, V, s);
-    token = descend<T>(row, r, 0, V, ask.place(all), s);
+    token = descend<T>(row, r, 0, V, (double)ask.u * part_sums<T>(row, r, 0, V, s), s);
   }
   answer<T>(a, j, row, token, f, n_top);
   __syncthreads();
