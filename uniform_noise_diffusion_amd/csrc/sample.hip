@@ -222,6 +222,7 @@ struct Row {
   double per;     // 256 log2(e) / T
   double far;     // from this distance on a weight is 2^-996
   int shift;      // a weight of 1 is 2^shift units
+  double most;    // and none is more units than this
   double min_w;   // min-p
   float below;    // logits under this one are certainly not kept
   uint32_t key;   // the cut: kept are larger keys, and this one up to `index`
@@ -229,8 +230,8 @@ struct Row {
   bool ties_only; // weights are 1 where the key is `key`, else 0
   const double* table;
   __device__ __forceinline__ Row(const Ask& ask, float top_, int V, const double* table_)
-      : top(top_), shift(0), min_w(ask.min_w), below(-kInf), key(0), index(V), ties_only(false),
-        table(table_) {
+      : top(top_), shift(0), most(0x1p62), min_w(ask.min_w), below(-kInf), key(0), index(V),
+        ties_only(false), table(table_) {
     // (T = inf: finite logits weigh 1, and -inf nothing all the same)
     per = ask.greedy ? 1.0 : 256.0 * 1.4426950408889634074 / fmin((double)ask.temp, 1e300);
     far = 256.0 * 996.0 / per;
@@ -244,6 +245,14 @@ struct Row {
   // `sum`: the weights that are summed as units, or a bound of them; they come to
   // 2^60 to 2^61 units at most
   __device__ __forceinline__ void scale(double sum) { shift = 60 - ilogb(fmax(sum, 1.0)); }
+  // Units for a draw at t, far under the row's weight: t is 2^40 to 2^41 of them,
+  // or kLeast's is the least unit, and a weight beyond t counts for 2^45 (of a
+  // list's 4,096 entries the sum is below 2^57).  The units that are to be passed.
+  __device__ __forceinline__ u64 refine(double t) {
+    shift = t > 0.0 ? min(990, 40 - ilogb(t)) : 990;
+    most = 0x1p45;
+    return (u64)ldexp(t, shift) + 1;
+  }
 };
 
 // A weight times 2^shift: 2^(-t / 256), t = (top - x) per, as the table's entry
@@ -277,7 +286,7 @@ __device__ __forceinline__ u64 to_units(double s) {  // s below 2^62
   return (u64)hi << 32 | lo;
 }
 __device__ __forceinline__ u64 units_of(const Row& r, float x) {
-  return to_units(scaled_weight(r, x, r.shift));
+  return to_units(fmin(scaled_weight(r, x, r.shift), r.most));
 }
 __device__ __forceinline__ bool within_cut(const Row& r, float x, int i) {
   const uint32_t k = key_of(x);
@@ -856,7 +865,7 @@ __device__ __forceinline__ u64 list_sum(const Row& r, int n, Shared& s) {
 // of 126,464, top-k and top-p: 32 us, and 45 where slots are searched, with two
 // passes over the list and a sort to each cut.  Looked at in pairs, longer lists
 // cost more: up to 512 entries, 256 rows' top-p would take 104 us instead of 75.)
-__device__ __forceinline__ int draw_from_few(const Ask& ask, const Row& r, int n, double all, Shared& s) {
+__device__ __forceinline__ int draw_from_few(const Ask& ask, Row r, int n, double all, Shared& s) {
   static_assert(kShort <= kThreads && 2 * kShort <= kFew, "a lane to an entry");
   ulonglong2* const pair = reinterpret_cast<ulonglong2*>(s.few);
   const int lanes = n <= kThreads / 4 ? 4 : n <= kThreads / 2 ? 2 : 1;
@@ -896,9 +905,15 @@ __device__ __forceinline__ int draw_from_few(const Ask& ask, const Row& r, int n
     if (goal == 0 || sum < goal) return -1;
     kept = kept && before < goal;
   }
-  const u64 left = kept && !(w < r.min_w) ? units : 0;
+  kept = kept && !(w < r.min_w);
+  u64 left = kept ? units : 0;
   const u64 sum = block_sum(q == 0 ? left : 0, s);
   if (sum == 0) return -1;
+  u64 goal = ask.place(sum) + 1;
+  if (ask.faint()) {  // (as in draw_from_list())
+    goal = r.refine((double)ask.u * ldexp((double)sum, -r.shift));
+    left = kept ? units_of(r, logit_of(e)) : 0;
+  }
   if (mine && q == 0) pair[i].y = left;
   __syncthreads();
   before = 0;
@@ -908,7 +923,6 @@ __device__ __forceinline__ int draw_from_few(const Ask& ask, const Row& r, int n
     before += (uint32_t)p.x < (uint32_t)e ? p.y : 0;
   }
   before = joined(before);
-  const u64 goal = ask.place(sum) + 1;
   if (mine && before < goal && goal <= before + left) s.pick[0] = (uint32_t)e;
   __syncthreads();
   return (int)s.pick[0];
@@ -930,10 +944,13 @@ __device__ __forceinline__ int draw_from_list(const Ask& ask, Row r, int n, doub
   r.min_w = min_w, r.below = fmaxf(r.below, below);
   const u64 sum = list_sum(r, n, s);
   if (sum == 0) return -1;
+  // (units of the whole are too coarse for a draw among its lightest tokens)
+  const u64 goal = ask.faint() ? r.refine((double)ask.u * ldexp((double)sum, -r.shift))
+                               : ask.place(sum) + 1;
   u64 e;
   const float per_slot = (float)kThreads / (float)V;
   find_entry(
-      s, n, ask.place(sum) + 1,
+      s, n, goal,
       [&](u64 x) { return min(kThreads - 1, (int)((float)(uint32_t)x * per_slot)); },
       [](u64 x) { return x << 32 | x >> 32; }, [&](u64 x) { return entry_units(r, x); }, &e);
   return (int)(uint32_t)e;
