@@ -490,16 +490,21 @@ struct Found {
 // NaN's, also of an infinite distance over an infinite T, becomes 0 by the
 // maximum).  A vector's terms are added in fp32, without those of the largest
 // logit so far, which are 1, and counted: next to a 1 what a decided row's
-// log-probability is made of would be lost.
+// log-probability is made of would be lost.  The multiply-add takes the largest
+// logit times log2(e) as fp32 rounds it; what that is off by, which grows with the
+// logits and not with their distances, is one power of two for all terms, and is
+// taken back where their sum is added.
 template <typename T, bool COUNT, bool ROUGH>
 __device__ __forceinline__ Found scan_part(const T* row, int lo, int hi, const Ask& ask,
                                            const Steps& steps, Scan& s) {
   constexpr int N = Vec<T>::n;
   Found f = {-kInf, 0.f, 0.0, 0};
   uint32_t ones = 0;
-  // log2(e) and the largest logit times it; the same over T.  Where that is near
-  // the end of float's range, any other logit's distance is past 2^x's, and the
-  // term is 0 (over T perhaps wrongly: the rough sum is then found too small).
+  // log2(e) and the largest logit times it (`back`: the power that undoes the
+  // product's rounding); the same over T.  From 2^30 on, no other logit is nearer
+  // than 64, and the term is 0 next to a 1; over T, near the end of float's range,
+  // perhaps wrongly: the rough sum is then found too small.
+  double back = 1.0;
   float mul = kLog2e, ref = 0.f, mul_t = ask.per_f, ref_t = 0.f;
   each_vec<T, 4>(row, lo, hi, [&](const float* v, int i) __attribute__((always_inline)) {
     const float most = most_of<N>(v);
@@ -513,8 +518,9 @@ __device__ __forceinline__ Found scan_part(const T* row, int lo, int hi, const A
         ones = 0;
         f.top = most;
         f.at = i;
-        const bool near = fabsf(most) < 1e37f, near_t = fabsf(most * ask.per_f) < 1e37f;
+        const bool near = fabsf(most) < 0x1p30f, near_t = fabsf(most * ask.per_f) < 1e37f;
         mul = near ? kLog2e : 0.f, ref = near ? most * kLog2e : 1000.f;
+        back = near ? (double)__builtin_amdgcn_exp2f(-fmaf(most, kLog2e, -ref)) : 1.0;
         mul_t = near_t ? ask.per_f : 0.f, ref_t = near_t ? most * ask.per_f : 1000.f;
       }
     }
@@ -527,7 +533,7 @@ __device__ __forceinline__ Found scan_part(const T* row, int lo, int hi, const A
       if (ROUGH) f.rough += fmaxf(0.f, __builtin_amdgcn_exp2f(fmaf(v[k], mul_t, -ref_t)));
       if (COUNT && i + k < hi) atomicAdd(&s.count[steps.of(v[k])], 1u);
     }
-    f.whole += (double)terms;
+    f.whole = fma((double)terms, back, f.whole);
   });
   f.whole += (double)ones;
   return f;
