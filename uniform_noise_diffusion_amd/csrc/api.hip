@@ -730,7 +730,7 @@ int mdlm_mx_product(const uint8_t* a, const uint8_t* a_exp, int32_t a_format, in
   const int64_t row_bytes = (a_format == MDLM_MX_E4M3 ? 32 : 16) * (((int64_t)H + 31) / 32);
   if (row_idx && n_tokens * row_bytes >= (int64_t)0xFFFFFFF0)
     return fail(MDLM_EUNSUPPORTED, "%s: listed rows need codes of less than 4 GiB", fn);
-  if (row_idx && n_rows)
+  if (row_idx)
     if (const int rc = check_row_list(fn, row_idx, nullptr, nullptr, n_rows, max_rows, n_tokens,
                                       V, st))
       return rc;

@@ -65,14 +65,14 @@ check_probs_kernel(const double* __restrict__ p, int32_t n_docs, int32_t* __rest
   report(bad, MDLM_CHECK_PROB, status);
 }
 
-// The row list of the fused head: the device row count within [0, max_rows],
-// and for every listed row its index in [0, n_tokens), its target in [0, V)
-// and a finite weight (tgt and w optional).
+// The row list of the fused head or the microscaled product: the device row
+// count within [0, max_rows] (null: max_rows), and for every listed row its index
+// in [0, n_tokens), its target in [0, V) and a finite weight (tgt and w optional).
 __global__ void __launch_bounds__(kThreads)
 check_rows_kernel(const int32_t* __restrict__ row_idx, const int32_t* __restrict__ tgt,
                   const float* __restrict__ w, const int32_t* __restrict__ n_rows_ptr,
                   int64_t max_rows, int64_t n_tokens, int32_t V, int32_t* __restrict__ status) {
-  const int32_t nr = *n_rows_ptr;
+  const int64_t nr = n_rows_ptr ? *n_rows_ptr : max_rows;
   if (blockIdx.x == 0 && threadIdx.x == 0 && (nr < 0 || nr > max_rows))
     atomicOr(status, MDLM_CHECK_ROW_COUNT);
   const int64_t n_rows = nr < 0 ? 0 : (nr > max_rows ? max_rows : nr);
