@@ -693,8 +693,9 @@ int mdlm_ckpt8_load(const uint8_t* q, const uint8_t* q_exp, int32_t dtype, int64
  *   rstd = 1 / sqrt(mean(sum_row^2) + eps),  y = sum * rstd * weight
  *
  * in fp32, the norm being that of the sum as it is kept; y rounded once, to
- * `dtype` and (from fp32) to the codes.  A row whose squares sum to more than
- * float's range has rstd 0.
+ * `dtype` and (from fp32) to the codes: one whose exact value lies within fp32's
+ * rounding of the border between two codes may become either.  A row whose
+ * squares sum to more than float's range has rstd 0.
  *
  *   x, residual [n, H] row-major, element type `dtype` (MDLM_BF16 or MDLM_F32).
  *   n, H        n >= 0 and below 2^31, H > 0; more than 16384 returns
@@ -759,7 +760,11 @@ enum { MDLM_MX_E2M1 = 4, MDLM_MX_E4M3 = 8 };
  * format's largest value, 448 or 6.  Dividing by it is exact, so an entry is off
  * by at most 2^-4 (e4m3) or 1/4 (e2m1) of itself, or by 2^-10 or 2^-2 times
  * 2^(b - 127) below the format's least normal value (one that rounds up past
- * the type's largest value comes back as an infinity).
+ * the type's largest value comes back as an infinity).  OCP's text leaves the
+ * scale to the writer; the conversion that it suggests takes the power of two of
+ * the largest magnitude itself and cuts what lies past the format's largest
+ * value.  Its bytes are one less than these wherever that would cut, and both
+ * are read alike.
  *   E4M3: infinities and NaN become NaN and do not touch the rest of their block
  *         (the scale is that of its finite entries).
  *   E2M1: a block with an infinity or NaN gets the byte 255 and is restored as
@@ -803,8 +808,9 @@ int mdlm_mx_dequantize(const uint8_t* q, const uint8_t* q_exp, int32_t format, i
  *               V at most 2^31 - 1024.
  *   row_idx     [max_rows] int32, the row of A for each row of logits (as
  *               mdlm_compact_rows lists them), or NULL: row j is j.  A row
- *               outside [0, n_tokens) gives zeros.  With row_idx, a must be
- *               smaller than 4 GiB.
+ *               outside [0, n_tokens) counts as one of zeros (its logits are
+ *               zeros, or NaN where a row of W holds NaN).  With row_idx, a must
+ *               be smaller than 4 GiB.
  *   n_rows      [1] int32 device word, rows to compute, or NULL: max_rows.
  *               Rows of logits from *n_rows on are left as they are.
  *   max_rows    0 .. 2^31 - 1024, the rows of `logits`; without row_idx at most
@@ -833,7 +839,8 @@ int mdlm_mx_product(const uint8_t* a, const uint8_t* a_exp, int32_t a_format, in
  *   min_p   of those, the tokens with w_i >= min_p.
  * token = the first one, by index, up to which the kept weights sum to more than
  * u times their sum.  logp = x_token - log(sum over i of exp(x_i)), the row's
- * own log-probability of it (temperature 1, nothing left out).
+ * own log-probability of it (temperature 1, nothing left out), from fp32 powers
+ * of the distances x_i - max x, added in fp64.
  *
  * Weights are formed and summed in fp64 (or as 64-bit integers), in an order that
  * the sizes determine: the same inputs give the same token.  A weight under

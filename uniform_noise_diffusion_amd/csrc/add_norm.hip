@@ -13,7 +13,8 @@
 // type or (from fp32) to e4m3 over the power of two of its block of 32.
 //
 // Memory is the bound: x and the residual are read once, s and y written once
-// (16,384 x 4,096 bf16 with 8-bit output: 94 us, 5.0 TB/s; one row: 2.8 us).
+// (16,384 x 4,096 bf16 with 8-bit output: 96 us, 4.9 TB/s; 8,192 x 12,288,
+// two eights to a lane and no prefetch, 144 us; one row: 2.8 us).
 // The layout is norm.hip's: a row's eights of columns dealt to W waves, NV to a
 // lane, the next row's loads issued before this one is reduced and written, and
 // no condition in the loop (with FULL, H a multiple of 8, lanes past the row's

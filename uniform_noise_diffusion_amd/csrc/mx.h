@@ -3,7 +3,8 @@
 //
 // The scale is the least power of two 2^e, e >= -127, under which the block's
 // largest magnitude is at most the format's largest value (448 or 6), kept as
-// the byte e + 127.  x / 2^e is exact in fp32, so the only rounding is the one
+// the byte e + 127: nothing is cut off, as it is where the scale is taken from the
+// magnitude's power of two alone.  x / 2^e is exact in fp32, so the only rounding is the one
 // to the format, to nearest even: every run and every implementation gets the
 // same bits.  Rows are padded to whole blocks with zero codes.
 //   e4m3: off by at most 2^-4 of the value (2^-10 * 2^e below 2^-6 * 2^e).  An

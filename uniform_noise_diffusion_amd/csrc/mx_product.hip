@@ -36,12 +36,16 @@
 // A persistent block sends for its next tile's first stage before it stores the
 // logits of this one, straight from the accumulators, and goes on while they drain.
 //
-// What bounds it.  Few rows: the reading of W, 48 us for one row of 126,464 x
-// 4,096 (275 MB, 5.8 TB/s).  Many rows: the matrix cores and the power they
-// draw.  From registers alone they reach 6.7 Pflop/s with random 4-bit rows, the
-// clock falling from 2.4 to 1.66 GHz, and 4.1 with 8-bit ones (2.0 GHz); 4,096
-// rows of 4,096 by 126,464 take 1,250 us (3.4 Pflop/s, 1.75 GHz, matrix cores
-// busy 44% of the cycles), 2,048 8-bit ones 1,014 us (2.1).  Of 1,308 us that the
+// What bounds it.  Few rows: the reading of W, 56 us for one 8-bit row of 126,464 x
+// 4,096 and 54 us for a 4-bit one (275 MB, 309 MB by the counters, 5.5 TB/s; 48 and
+// 46 us with the same head again and again, part of which the Infinity Cache then
+// holds).  Many rows: waiting.  From registers alone the matrix cores reach 6.7
+// Pflop/s with random 4-bit rows, kept busy throughout while their power takes the
+// clock from 2.4 to 1.66 GHz, and 4.1 with 8-bit ones (2.0 GHz); 4,096 rows of
+// 4,096 by 126,464 take 1,260 us (3.4 Pflop/s), matrix cores busy 45% of the cycles
+// at 1.78 GHz, 2,048 8-bit ones 1,014 us (2.1).  Each stage's barrier waits for all
+// of the next stage's loads, and the block is the only one on its CU.  8-bit rows
+// bring twice the bytes for a product, through LDS too.  Of 1,308 us that the
 // first took when its logits still passed through LDS, 860 were left without any
 // load and LDS read, 930 with the exponents', 980 with LDS reads but no loads,
 // 1,190 with loads but no LDS reads; larger tiles per wave (a third fewer LDS
@@ -461,7 +465,7 @@ void run(const MxProductArgs& a, int per_cu, hipStream_t stream) {
 // The tile.  Up to 64 rows the time is the reading of W, and a tile has them
 // all: blocks of two waves where W is small, so that every CU has some (4,096 x
 // 4,096, 64 rows: 9 us, with eight waves 15), else of eight (1 row, 126,464 x
-// 4,096: 48 us, 5.8 TB/s).  Beyond, 256 rows of W by 256 of A (128 of 8-bit ones)
+// 4,096: 56 us, 5.5 TB/s).  Beyond, 256 rows of W by 256 of A (128 of 8-bit ones)
 // move the fewest bytes into LDS for a product, but a CU holds one block of them.
 // 128 x 128 is taken where one round of blocks does it all, or where half of
 // the large tile would be past the last row; both measured, 4,096 x 4,096 but

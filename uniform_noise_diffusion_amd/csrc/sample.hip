@@ -43,13 +43,17 @@
 // Few rows are cut into segments, a block each, for both passes; the second
 // kernel then draws from what they leave.
 //
-// What bounds it.  1,024 rows of 262,144 bf16 logits with min-p take 193 us, for
-// two readings of 537 MB that memory gives at 5.7 TB/s; of 126,464 fp32 logits
-// with top-k 170 us (as bounded), with top-p 285 us, for the vector units: every
-// logit then has a term, a count and an fp64 weight.  One row of 126,464 takes 32
-// us, in four launches, for the latencies of the steps from one to the next.
+// What bounds it.  1,024 rows of 262,144 bf16 logits with min-p take 195 us, for
+// two readings of 537 MB that memory gives at 6.0 TB/s; of 126,464 fp32 logits
+// with top-k 165 us (as bounded), with top-p 282 us, for the vector units: every
+// logit then has a term, a count and an fp64 weight; with temperature alone 190 us
+// (an fp64 weight for each); greedy 97 us, in one reading.  Rows whose top-p cut
+// lies too deep for the list and that min-p cuts too are the second kernel's: 800
+// to 1,050 us.  One row of 126,464 takes 28 us, in four launches, for the latencies
+// of the steps from one to the next.  Short rows take a block each for its fixed
+// work: 4,096 rows of 1,000 bf16 74 us, with top-p 170 us.
 // Every function here is inlined: what calls save of the registers was 64 KB of
-// scratch memory a row (1,024 rows with top-k took 205 us).
+// scratch memory a row (1,024 rows with top-k took 205 us and not 170).
 #include <math.h>
 
 #include <algorithm>
@@ -868,7 +872,7 @@ __device__ __forceinline__ u64 list_sum(const Row& r, int n, Shared& s) {
 // draw_from_list() for at most kShort entries: an entry's place in the order, what
 // lies before it and, of what is kept, what lies before it by index are counted by
 // looking at every other one, each entry by as many lanes as there are.  (One row
-// of 126,464, top-k and top-p: 32 us, and 45 where slots are searched, with two
+// of 126,464, top-k and top-p: 32 us then, and 45 where slots are searched, with two
 // passes over the list and a sort to each cut.  Looked at in pairs, longer lists
 // cost more: up to 512 entries, 256 rows' top-p would take 104 us instead of 75.)
 __device__ __forceinline__ int draw_from_few(const Ask& ask, Row r, int n, double all, Shared& s) {
