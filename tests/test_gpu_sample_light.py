@@ -96,3 +96,22 @@ def test_first_tokens_of_a_large_top_k(dtype, spread, k):
     few_and_many(x, u, top_k=np.full(m, k))
     few_and_many(x, u, top_k=np.full(m, k), top_p=np.full(m, 0.999999))
     few_and_many(x, u, top_k=np.full(m, k), min_p=np.full(m, 1e-30))
+
+
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("tops", [2, 8])
+@pytest.mark.parametrize("width", [40, 4000, V])
+@pytest.mark.parametrize("kw", [dict(), dict(top_k=3000), dict(top_k=9000)])
+def test_borders_between_equal_tops(dtype, tops, width, kw):
+    """u on the border between two of some equal logits, `width` apart at most, all
+    else 180 and more under them: next to those it adds nothing to a sum, and the draw
+    is the next of them."""
+    rng = RNG(tops + width)
+    m = tops - 1
+    x = -rng.uniform(180, 600, (m, V))
+    x[rng.random((m, V)) < 0.2] = -np.inf
+    for i in range(m):
+        x[i, rng.integers(0, V - width + 1) + rng.choice(width, tops, replace=False)] = 0.0
+    x = torch.from_numpy(x).to(dtype).to(DEV)
+    u = (np.arange(1, tops) / tops).astype(np.float32)
+    few_and_many(x, u, **{k: np.full(m, v) for k, v in kw.items()})

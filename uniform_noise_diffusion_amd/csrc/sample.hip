@@ -994,30 +994,40 @@ __device__ __forceinline__ double part_sums(const T* row, const Row& r, int lo, 
                      s);
 }
 
-// Where t falls among `n` parts of these weights: the first one up to which they
-// sum to more than t, or the last that weighs anything (a sum taken in another
-// order may leave t no less than the whole), and in *t what of it lies in that
-// part.  -1: none weighs anything.
-__device__ __forceinline__ int part_at(const double* weight, int n, double* t) {
-  double before = 0.0, upto = 0.0;
+// The largest number below x > 0.
+__device__ __forceinline__ double just_below(double x) {
+  return __longlong_as_double(__double_as_longlong(x) - 1);
+}
+
+// Where *t falls among `n` parts of these weights, *before lying before them: the
+// first one up to which all of it sums to more than *t, and in *before what lies
+// before that part.  -1: none weighs anything.  Sums taken in different orders may
+// leave *t no less than the whole; it is then taken just below.  (Sums start at the
+// row's first token all the way down: were what lies before taken off t, a draw on
+// the border between two equal tokens would fall to the least one between them.)
+__device__ __forceinline__ int part_at(const double* weight, int n, double* t, double* before) {
+  double upto = *before;
+  for (int k = 0; k < n; ++k) upto += weight[k];
+  *t = fmin(*t, just_below(upto));
   int part = -1;
-  for (int k = 0; k < n && !(upto > *t); ++k) {
+  upto = *before;
+  for (int k = 0; k < n && (part < 0 || !(upto > *t)); ++k) {
     if (!(weight[k] > 0.0)) continue;
-    part = k, before = upto, upto += weight[k];
+    part = k, *before = upto, upto += weight[k];
   }
-  *t = fmax(*t - before, 0.0);
   return part;
 }
 
-// The first token of [lo, hi) up to which the kept weights sum to more than t
-// (the last kept one at most); -1: none is kept.
+// The first token of [lo, hi) up to which the kept weights, and `before`, sum to
+// more than t (or to as much as they come to); -1: none is kept.
 template <typename T>
-__device__ __forceinline__ int descend(const T* row, const Row& r, int lo, int hi, double t, Shared& s) {
+__device__ __forceinline__ int descend(const T* row, const Row& r, int lo, int hi, double t,
+                                       double before, Shared& s) {
   constexpr int N = Vec<T>::n;
   const int lane = threadIdx.x & 63;
   while (hi - lo > 64 * N) {
     part_sums<T>(row, r, lo, hi, s);
-    const int w = part_at(s.weigh, kWaves, &t);
+    const int w = part_at(s.weigh, kWaves, &t, &before);
     if (w < 0) {
       __syncthreads();
       return -1;
@@ -1036,10 +1046,16 @@ __device__ __forceinline__ int descend(const T* row, const Row& r, int lo, int h
     sum += mine[k];
   }
   const double upto = scan64(sum);
-  double before = __shfl_up(upto, 1, 64);
-  if (lane == 0) before = 0.0;
+  const double last = __shfl_up(upto, 1, 64);
+  if (lane > 0) before += last;
   // (sums round: a token is taken only if it weighs something itself)
-  const u64 any = __ballot(sum > 0.0), hit = __ballot(sum > 0.0 && upto > t);
+  double end = before;
+#pragma unroll
+  for (int k = 0; k < N; ++k) end += mine[k];
+  double most = sum > 0.0 ? end : 0.0;
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) most = fmax(most, __shfl_xor(most, d, 64));
+  t = fmin(t, just_below(most));
   int at = -1;
   bool past = false;
 #pragma unroll
@@ -1047,19 +1063,22 @@ __device__ __forceinline__ int descend(const T* row, const Row& r, int lo, int h
     before += mine[k];
     if (mine[k] > 0.0 && !past) at = i + k, past = before > t;
   }
+  const u64 hit = __ballot(past);
   __syncthreads();
-  return any ? __shfl(at, hit ? __ffsll(hit) - 1 : 63 - __clzll((long long)any), 64) : -1;
+  return hit ? __shfl(at, __ffsll(hit) - 1, 64) : -1;
 }
 
-// Where u falls among the row's `n` parts of these weights: the part, and in *t
-// what of it lies there.  -1, and *t in the whole row, where u's place is so near
+// Where u falls among the row's `n` parts of these weights: its place *t, the part,
+// and *before, what lies before that.  -1, the whole row, where u's place is so near
 // the row's start that what the parts leave out (a list's units, what is
 // kLeast or less) could decide.
-__device__ __forceinline__ int part_of(const Ask& ask, const double* weight, int n, double* t) {
+__device__ __forceinline__ int part_of(const Ask& ask, const double* weight, int n, double* t,
+                                       double* before) {
   double all = 0.0;
   for (int k = 0; k < n; ++k) all += weight[k];
   *t = (double)ask.u * all;
-  return ask.faint() ? -1 : part_at(weight, n, t);
+  *before = 0.0;
+  return ask.faint() ? -1 : part_at(weight, n, t, before);
 }
 
 // Writes a row's answer.  n_top: how many logits are infinite, if any is.
@@ -1159,11 +1178,11 @@ sample_row_kernel(const SampleArgs a, RowState* __restrict__ states) {
       parts = true;
     }
     if (parts) {
-      double t;
+      double t, before;
       int lo = 0, hi = V;
-      const int part = part_of(ask, s.weigh, kWaves, &t);
+      const int part = part_of(ask, s.weigh, kWaves, &t, &before);
       if (part >= 0) share<T>(part, 0, V, &lo, &hi);
-      token = descend<T>(row, r, lo, hi, t, s);
+      token = descend<T>(row, r, lo, hi, t, before, s);
     }
     if (token < 0) route = kGeneral;
   }
@@ -1335,11 +1354,11 @@ sample_third_kernel(const SampleArgs a, RowState* __restrict__ states, const Seg
     if (threadIdx.x < kMaxSegments)
       weight[threadIdx.x] += ldexp((double)units[threadIdx.x], -r.shift);
     __syncthreads();
-    double t;
+    double t, before;
     int lo = 0, hi = V;
-    const int k = part_of(ask, weight, g.per_row, &t);
+    const int k = part_of(ask, weight, g.per_row, &t, &before);
     if (k >= 0) lo = min(V, k * g.size), hi = min(V, lo + g.size);
-    token = descend<T>(row, r, lo, hi, t, s);
+    token = descend<T>(row, r, lo, hi, t, before, s);
   }
   if (threadIdx.x == 0) states[j].route = token < 0 ? kGeneral : kDone;
   if (token >= 0) answer<T>(a, j, row, token, f, 0);
@@ -1471,7 +1490,8 @@ __device__ __forceinline__ void cut(const T* row, Row& r, const Ask& ask, bool b
     ties.below = value_of(in.prefix);
     const u64 each = by_count ? 1 : units_of(r, value_of(in.prefix));
     const u64 n = each ? (need + each - 1) / each : inside;
-    r.index = descend<T>(row, ties, 0, V, (double)(max((u64)1, min(n, inside)) - 1), s);
+    r.index = descend<T>(row, ties, 0, V, (double)(max((u64)1, min(n, inside)) - 1), 0.0,
+                         s);
     r.key = in.prefix;
     r.below = fmaxf(r.below, ties.below);
     return;
@@ -1512,7 +1532,7 @@ __device__ __forceinline__ void rest_of_row(const SampleArgs& a, int64_t j, cons
     u64 n = ask.greedy ? 1 : n_top;
     if (ask.by_k) n = min(n, (u64)ask.k);
     if (ask.by_p) n = ask.goal(n);
-    token = descend<T>(row, r, 0, V, (double)ask.u * (double)n, s);
+    token = descend<T>(row, r, 0, V, (double)ask.u * (double)n, 0.0, s);
   } else {
     const double min_w = r.min_w;
     const float below = r.below;
@@ -1530,7 +1550,8 @@ __device__ __forceinline__ void rest_of_row(const SampleArgs& a, int64_t j, cons
     }
     if (ask.by_p) cut<T>(row, r, ask, false, ask.by_k ? ask.goal(all) : 0, V, s);
     r.min_w = min_w, r.below = fmaxf(r.below, below);
-    token = descend<T>(row, r, 0, V, (double)ask.u * part_sums<T>(row, r, 0, V, s), s);
+    const double t = (double)ask.u * part_sums<T>(row, r, 0, V, s);
+    token = descend<T>(row, r, 0, V, t, 0.0, s);
   }
   answer<T>(a, j, row, token, f, n_top);
   __syncthreads();
