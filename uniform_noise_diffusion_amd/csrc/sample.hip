@@ -46,12 +46,12 @@
 // What bounds it.  1,024 rows of 262,144 bf16 logits with min-p take 195 us, for
 // two readings of 537 MB that memory gives at 6.0 TB/s; of 126,464 fp32 logits
 // with top-k 165 us (as bounded), with top-p 282 us, for the vector units: every
-// logit then has a term, a count and an fp64 weight; with temperature alone 190 us
+// logit then has a term, a count and an fp64 weight; with temperature alone 186 us
 // (an fp64 weight for each); greedy 97 us, in one reading.  Rows whose top-p cut
-// lies too deep for the list and that min-p cuts too are the second kernel's: 800
-// to 1,050 us.  One row of 126,464 takes 28 us, in four launches, for the latencies
+// lies too deep for the list and that min-p cuts too are the second kernel's: 790
+// to 1,040 us.  One row of 126,464 takes 28 us, in four launches, for the latencies
 // of the steps from one to the next.  Short rows take a block each for its fixed
-// work: 4,096 rows of 1,000 bf16 74 us, with top-p 170 us.
+// work: 4,096 rows of 1,000 bf16 78 us, with top-p 171 us.
 // Every function here is inlined: what calls save of the registers was 64 KB of
 // scratch memory a row (1,024 rows with top-k took 205 us and not 170).
 #include <math.h>
